@@ -297,6 +297,130 @@ W8A8_API int w8a16_linear(const void *x_bf16, int64_t M, int64_t K, int64_t ldx,
                           int64_t N, void *y_bf16, int64_t ldy, w8a8_stream_t stream);
 
 /*
+ * The layer's gradient with respect to its input, for training through a
+ * frozen int8 layer.  With the dequantized weight Wq[n,k] * s_w[n] (the
+ * rounding of x to int8 passes the gradient straight through), dy bf16 [M,N]
+ * (row stride lddy) -> dx bf16 [M,K] (row stride lddx):
+ *
+ *   g[m,n]  = dy[m,n] * s_w[n]                           (fp32, RNE)
+ *   s_g[m]  = max_n |g[m,n]| / 127                       (fp32, IEEE, RNE)
+ *   c[m,n]  = clamp(rint(g[m,n] / s_g[m]), -127, 127)    (a row of zeros: 0)
+ *   dx[m,k] = bf16_rne( (float)(sum_n c[m,n] * Wq[n,k]) * s_g[m] )
+ *
+ * the sum exact in int32.  The channel scales lie along the contraction, so
+ * they enter the rows before these are quantized per token.  Wq is read as it
+ * is stored (no transposed copy).  Preconditions as for w8a8_linear_fused,
+ * with N <= 133144 (132104 with codes of -128) as the length of the sum and
+ * lddy, lddx multiples of 8.  variant: a w8a8_variant; AUTO chooses.  GEMV
+ * and GEMM_BN64 have no such form (W8A8_ERR_UNSUPPORTED_SHAPE), GEMV_TC serves
+ * M <= 128.  workspace: w8a8_input_grad_workspace_size bytes, 16-byte aligned
+ * (codes and row scales, required, and the K-split region of w8a8_linear,
+ * optional); no initialization is needed.
+ */
+W8A8_API int w8a8_input_grad_workspace_size(int64_t M, int64_t N, int64_t K, int variant,
+                                            size_t *bytes);
+W8A8_API int w8a8_linear_input_grad(const void *dy_bf16, int64_t M, int64_t N, int64_t lddy,
+                                    const int8_t *Wq, const float *s_w, int64_t K, void *dx_bf16,
+                                    int64_t lddx, int variant, void *workspace, size_t ws_bytes,
+                                    w8a8_stream_t stream);
+
+/* Value types of the operators below (the layer itself takes bf16). */
+typedef enum { W8A8_DTYPE_BF16 = 0, W8A8_DTYPE_FP16 = 1, W8A8_DTYPE_FP32 = 2 } w8a8_dtype;
+
+/* Which values of a head form pair i of `rot` rotated values. */
+typedef enum {
+    W8A8_ROTARY_INTERLEAVED = 0,  /* 2i and 2i + 1 */
+    W8A8_ROTARY_HALF = 1          /* i and i + rot / 2 */
+} w8a8_rotary_layout;
+
+/* The heads of one tensor, [batch, tokens, heads, dim] with adjacent values
+ * in a head and any strides (in elements) otherwise; x strides may be 0 (a
+ * broadcast input), y strides of extents above 1 may not. */
+typedef struct {
+    const void *x;
+    void *y;
+    int64_t heads;
+    int64_t x_batch, x_token, x_head;
+    int64_t y_batch, y_token, y_head;
+} w8a8_rotary_heads;
+
+/*
+ * Rotary positions on the heads that a projection wrote (for a fused q|k|v
+ * layer: strided views of its output), for one tensor or for q and k in one
+ * launch.  Pair i = (a, b) of the first `rot` values of a head at position p:
+ *   a' = scale * (a cos t - b sin t),  b' = scale * (a sin t + b cos t),
+ *   t = p[axis[i]] * inv_freq[i];
+ * the other dim - rot values are copied.  backward != 0: the gradient of that
+ * map, its transpose (t -> -t).  Rotations are fp32, rounded once; angles are
+ * reduced exactly as 64-bit fixed-point turns, so far positions lose nothing.
+ * positions: device integers of position_bits (32 or 64) bits, signed,
+ * [batch, tokens, axes] with strides pos_batch and pos_token (in elements, 0
+ * to share) and adjacent axes; axes 1..8.  inv_freq: HOST array of rot / 2
+ * radians per position (finite, >= 0), any scaling for long contexts applied;
+ * axis: HOST array of rot / 2 axis indices, or NULL (all 0).  Both are read
+ * before the call returns.
+ * y is x itself with the same strides, or does not overlap it.  dim and rot
+ * even, rot <= dim <= 512, batch * tokens < 2^30.  Accesses are 16 bytes wide
+ * where pointers, strides, dim and rot allow, else single values.
+ */
+W8A8_API int w8a8_rotary(const w8a8_rotary_heads *tensors, int num_tensors, int dtype,
+                         int64_t batch, int64_t tokens, int64_t dim, int64_t rot, int layout,
+                         const void *positions, int position_bits, int64_t pos_batch,
+                         int64_t pos_token, int64_t axes, const double *inv_freq,
+                         const int32_t *axis_or_null, float scale, int backward,
+                         w8a8_stream_t stream);
+
+/* Activations of the group norm. */
+typedef enum { W8A8_ACT_NONE = 0, W8A8_ACT_SILU = 1 } w8a8_activation;
+
+/*
+ * Group normalization of channels-last tensors, ahead of the int8 layers whose
+ * rows are an image's pixels.  x [B, S, C] (S pixels, adjacent channels; strides
+ * of a sample and a pixel in elements), G groups of C / G adjacent channels:
+ *   mean, var over a sample's S * C / G values of a group (fp32, var biased),
+ *   z = (x - mean) / sqrt(var + eps) * weight[c] + bias[c],  y = z, or
+ *   z * sigmoid(z) with W8A8_ACT_SILU; fp32 throughout, rounded once.
+ * weight, bias: [C] in x's type or fp32 (param_dtype), or NULL (1 and 0).
+ * mean_out, rstd_out: fp32 [B, G], or both NULL.
+ * w8a8_group_norm: y in x's type; it may be x itself with the same strides.
+ * w8a8_group_norm_quant: x bf16, C % 16 == 0; the rows of y (fp32, not
+ * rounded to bf16 first) quantized as w8a8_quant_act does: q int8 [B * S, C]
+ * dense and s_a fp32 [B * S], the operand of w8a8_linear.
+ * w8a8_group_norm_backward: from dy, x and the forward's mean and rstd,
+ *   dz = dy * y'(z),  dbias = sum dz,  dweight = sum dz * xh  (fp32 [C], or
+ *   NULL),  dx = (weight dz - E(weight dz) - xh E(weight dz xh)) * rstd
+ * with xh = (x - mean) * rstd and E over the group; dx in x's type, which may
+ * be dy or x itself with the same strides.  Sums run in a fixed order: equal
+ * inputs give equal bits.
+ * C % 8 == 0, C <= 4096 (2048 in fp32), strides multiples of 8 and at least
+ * C where their extent is above 1, B * S < 2^30, x, dy, y, q 16-byte aligned.
+ * workspace: w8a8_group_norm_workspace_size bytes, 16-byte aligned, no
+ * initialization needed.
+ */
+W8A8_API int w8a8_group_norm_workspace_size(int64_t B, int64_t S, int64_t C, int64_t G, int dtype,
+                                            int backward, size_t *bytes);
+W8A8_API int w8a8_group_norm(const void *x, int64_t x_batch, int64_t x_pixel, int dtype, int64_t B,
+                             int64_t S, int64_t C, int64_t G, const void *weight_or_null,
+                             const void *bias_or_null, int param_dtype, float eps, int activation,
+                             void *y, int64_t y_batch, int64_t y_pixel, float *mean_out_or_null,
+                             float *rstd_out_or_null, void *workspace, size_t ws_bytes,
+                             w8a8_stream_t stream);
+W8A8_API int w8a8_group_norm_quant(const void *x_bf16, int64_t x_batch, int64_t x_pixel, int64_t B,
+                                   int64_t S, int64_t C, int64_t G, const void *weight_or_null,
+                                   const void *bias_or_null, int param_dtype, float eps,
+                                   int activation, int8_t *q, float *s_a, float *mean_out_or_null,
+                                   float *rstd_out_or_null, void *workspace, size_t ws_bytes,
+                                   w8a8_stream_t stream);
+W8A8_API int w8a8_group_norm_backward(const void *dy, int64_t dy_batch, int64_t dy_pixel,
+                                      const void *x, int64_t x_batch, int64_t x_pixel, int dtype,
+                                      int64_t B, int64_t S, int64_t C, int64_t G, const float *mean,
+                                      const float *rstd, const void *weight_or_null,
+                                      const void *bias_or_null, int param_dtype, int activation,
+                                      void *dx, int64_t dx_batch, int64_t dx_pixel,
+                                      float *dweight_or_null, float *dbias_or_null,
+                                      void *workspace, size_t ws_bytes, w8a8_stream_t stream);
+
+/*
  * Host-only: the selector's plan for (M, N, K) on a device with num_sms SMs
  * (148 on B200).  Pure function of its arguments; needs no GPU.
  */

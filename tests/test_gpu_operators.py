@@ -1,0 +1,605 @@
+"""Rotary positions, group norm and the layer's input gradient on the GPU,
+against plain implementations in 64 bits.
+
+Tolerances count roundings: an output is rounded once (half a step of its
+type), and the fp32 work ahead of it is off by a stated number of units of
+2^-24 of the terms it adds.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import w8a8_int8_dynamic_token_b200 as w8a8
+from w8a8_int8_dynamic_token_b200 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24  # half a step of fp32, relative
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from w8a8_int8_dynamic_token_b200 import build
+    build.build()
+    torch.cuda.set_device(0)
+    yield
+    assert w8a8.last_device_error() == B.W8A8_OK
+
+
+def rounding(value64, dtype):
+    """Half a step of `dtype` at a 64-bit value."""
+    f = torch.finfo(dtype)
+    return value64.abs().clamp_min(f.tiny) * (f.eps / 2)
+
+
+def close(got, want64, slack64, what):
+    """|got - want| <= slack + half a step at |want| + slack."""
+    got = got.detach().cpu()
+    err = (got.double() - want64).abs()
+    tol = slack64 + rounding(want64.abs() + slack64, got.dtype)
+    assert torch.isfinite(got.double()).all(), f"{what}: not finite"
+    bad = err > tol
+    assert not bad.any(), f"{what}: {int(bad.sum())} values off, worst {float((err / tol).max()):.3g} of the tolerance"
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# ----------------------------------------------------------------- rotary
+
+# cos and sin: the angle's 32 bits to fp32 (pi 2^-25), its cut at 2^-32 turns,
+# one step of sincospif and the product with scale; then one product and one
+# fused product, rounded: below 2^-21 of (|a| + |b|) * scale together.
+ROT_SLACK = 2.0 ** -21
+
+
+def rotary64(x, pos, freq, layout, axis, scale, backward):
+    """x [B, T, H, D] and pos [B, T, A] on the CPU -> (y, slack), 64 bits."""
+    rot = 2 * len(freq)
+    ang = pos.double()[..., axis.long()] * freq           # [B, T, rot / 2]
+    ang = -ang if backward else ang
+    c, s = ang.cos()[:, :, None], ang.sin()[:, :, None]
+    y = x.double().clone()
+    slack = torch.zeros_like(y)
+    ia, ib = ((slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half"
+              else (slice(0, rot, 2), slice(1, rot, 2)))
+    a, b = x.double()[..., ia], x.double()[..., ib]
+    y[..., ia] = scale * (a * c - b * s)
+    y[..., ib] = scale * (a * s + b * c)
+    slack[..., ia] = slack[..., ib] = ROT_SLACK * scale * (a.abs() + b.abs())
+    return y, slack
+
+
+ROT_CASES = [
+    # batch, tokens, heads, kv heads, dim, rot, layout, axes, dtype, storage
+    (1, 1, 1, None, 2, 2, "half", 1, torch.bfloat16, "tokens"),
+    (1, 1, 32, 8, 128, 128, "half", 1, torch.bfloat16, "tokens"),
+    (1, 37, 3, 3, 128, 128, "interleaved", 3, torch.bfloat16, "qkv"),
+    (2, 53, 5, 1, 80, 40, "half", 1, torch.float16, "heads"),      # 16-byte units do not divide
+    (2, 53, 5, 1, 80, 40, "interleaved", 1, torch.float16, "heads"),
+    (3, 65, 4, 2, 256, 64, "half", 1, torch.float32, "heads"),
+    (1, 700, 2, None, 64, 64, "interleaved", 1, torch.float32, "qkv"),
+    (1, 19, 7, 2, 96, 32, "interleaved", 2, torch.bfloat16, "tokens"),
+    (1, 5, 2, 1, 512, 512, "half", 1, torch.bfloat16, "tokens"),
+    (1, 5, 2, 1, 512, 510, "half", 1, torch.float32, "tokens"),    # odd number of pairs
+    (1, 11, 3, 2, 6, 4, "interleaved", 1, torch.float16, "odd"),   # rows off 16 bytes
+    (1, 11, 300, 1, 16, 16, "half", 1, torch.bfloat16, "odd"),
+    (4, 1, 9, 3, 128, 64, "half", 8, torch.bfloat16, "tokens"),
+]
+
+
+def make_heads(b, t, h, kv, d, dtype, storage, seed):
+    g = gen(seed)
+    kv = kv or 0
+    if storage == "qkv":
+        both = torch.randn((b, t, h + 2 * kv, d), generator=g).to(dtype)
+        dev = both.cuda()
+        return both[:, :, :h], both[:, :, h:h + kv], dev[:, :, :h], dev[:, :, h:h + kv]
+    if storage == "odd":  # rows of h * d + 1 values
+        both = torch.randn((b, t, (h + kv) * d + 1), generator=g).to(dtype)
+        dev = both.cuda()
+        cut = lambda v, lo, n: v[..., 1 + lo * d:1 + (lo + n) * d].unflatten(-1, (n, d))  # noqa: E731
+        return cut(both, 0, h), cut(both, h, kv), cut(dev, 0, h), cut(dev, h, kv)
+    q = torch.randn((b, t, h, d), generator=g).to(dtype)
+    k = torch.randn((b, t, kv, d), generator=g).to(dtype)
+    if storage == "heads":
+        return q, k, q.transpose(1, 2).contiguous().cuda().transpose(1, 2), \
+            k.transpose(1, 2).contiguous().cuda().transpose(1, 2)
+    return q, k, q.cuda(), k.cuda()
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("b,t,h,kv,d,rot,layout,axes,dtype,storage", ROT_CASES)
+def test_rotary(b, t, h, kv, d, rot, layout, axes, dtype, storage, backward):
+    q, k, qd, kd = make_heads(b, t, h, kv, d, dtype, storage, 1)
+    freq = torch.rand(rot // 2, generator=gen(2), dtype=torch.float64)
+    axis = torch.randint(0, axes, (rot // 2,), generator=gen(3), dtype=torch.int32)
+    pos = torch.randint(-5000, 100000, (b, t, axes), generator=gen(4))
+    scale = 1.25
+    posd = pos.cuda() if axes > 1 else pos[..., 0].cuda()
+    if t % 2:  # 32-bit positions in half of the cases
+        posd = posd.int()
+    got = w8a8.rotary(qd, posd, freq, k=kd if kv else None, layout=layout,
+                      axis=axis if axes > 1 else None, scale=scale, backward=backward)
+    yq, yk = got if kv else (got, None)
+    for x, y, name in ((q, yq, "q"), (k, yk, "k")):
+        if y is None:
+            continue
+        want, slack = rotary64(x, pos, freq, layout, axis, scale, backward)
+        close(y, want, slack, name)
+        assert torch.equal(y[..., rot:].cpu(), x[..., rot:])  # copied bit for bit
+
+
+def test_rotary_far_positions_and_a_shared_row_of_them():
+    # positions up to 2^31 and beyond: the fixed-point turns are off by at most
+    # |pos| 2^-65 turns plus the frequency's own rounding to 53 bits, which the
+    # 64-bit product below has too
+    pos = torch.tensor([0, 1, -1, 2 ** 20 + 1, 2 ** 31 - 1, -2 ** 31, 2 ** 33 + 7])
+    freq = w8a8.rotary_frequencies(64, 1000000.0)[0]
+    x = torch.randn((3, len(pos), 2, 64), generator=gen(5))
+    y = w8a8.rotary(x.cuda(), pos.cuda(), freq, layout="half")  # [tokens], shared by the batch
+    # exact turns in whole numbers
+    turns = torch.tensor([[p * int(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 / 2.0 ** 64 for f in freq.tolist()]
+                          for p in pos.tolist()], dtype=torch.float64) * (2 * math.pi)
+    c, s = turns.cos()[None, :, None], turns.sin()[None, :, None]
+    a, b = x[..., :32].double(), x[..., 32:].double()
+    slack = ROT_SLACK * (a.abs() + b.abs())
+    close(y[..., :32], a * c - b * s, slack, "a")
+    close(y[..., 32:], a * s + b * c, slack, "b")
+
+
+def test_rotary_in_place_partial_and_out():
+    freq = w8a8.rotary_frequencies(32)[0]
+    x = torch.randn((9, 4, 64), generator=gen(6)).bfloat16().cuda()
+    pos = torch.arange(9, device="cuda")
+    want = w8a8.rotary(x, pos, freq)
+    big = torch.full((9, 6, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = big[:, 1:5]
+    assert w8a8.rotary(x, pos, freq, out=out) is out
+    assert torch.equal(out, want)
+    assert (big[:, 0] == 7).all() and (big[:, 5] == 7).all()  # neighbours are left alone
+    same = x.clone()
+    assert w8a8.rotary(same, pos, freq, out=same) is same
+    assert torch.equal(same, want)
+
+
+def test_rotary_broadcast_input():
+    freq = w8a8.rotary_frequencies(16)[0]
+    x = torch.randn((7, 1, 16), generator=gen(7)).cuda().expand(7, 5, 16)
+    pos = torch.arange(7, device="cuda", dtype=torch.int32)
+    y = w8a8.rotary(x, pos, freq)
+    assert torch.equal(y, w8a8.rotary(x.contiguous(), pos, freq))
+
+
+def test_rotary_gradient_is_the_transpose():
+    # <u, R x> = <R^T u, x> up to the roundings of both sides
+    freq = w8a8.rotary_frequencies(64, scaling="ramp", factor=8.0, trained=512)
+    x, u = (torch.randn((2, 33, 3, 64), generator=gen(s)) for s in (8, 9))
+    pos = torch.arange(33, device="cuda") * 37
+    y = w8a8.rotary(x.cuda(), pos, freq[0], scale=freq[1]).cpu().double()
+    g = w8a8.rotary(u.cuda(), pos, freq[0], scale=freq[1], backward=True).cpu().double()
+    left, right = (y * u.double()).sum(), (g * x.double()).sum()
+    # per value: slack of (|a| + |b|) <= 2 max and half a step
+    bound = (ROT_SLACK + U) * freq[1] * 2 * (x.abs().max() * u.abs().double().sum() + u.abs().max() * x.abs().double().sum())
+    assert abs(left - right) <= bound
+
+
+# ----------------------------------------------------------------- group norm
+
+def norm64(x, G, w, b, eps, silu):
+    """x [B, S, C] -> (y, mean, rstd, z, xhat), 64 bits."""
+    Bn, S, C = x.shape
+    xg = x.double().view(Bn, S, G, C // G)
+    mean = xg.mean((1, 3))
+    var = ((xg - mean[:, None, :, None]) ** 2).mean((1, 3))
+    rstd = 1.0 / torch.sqrt(var + eps)
+    xhat = ((xg - mean[:, None, :, None]) * rstd[:, None, :, None]).view(Bn, S, C)
+    z = xhat
+    if w is not None:
+        z = z * w.double()
+    if b is not None:
+        z = z + b.double()
+    y = z * torch.sigmoid(z) if silu else z
+    return y, mean, rstd, z, xhat
+
+
+def chain(S, C):
+    """Roundings one after another in a statistic, at most: batches of 8 pixels
+    joined one by one in a thread (no slab is longer than S pixels over 148
+    blocks, or than one batch per thread), sums within a batch, the joins."""
+    return math.ceil(S / 148 / 8) + 8 + 24
+
+
+def norm_slack(x, y, mean, rstd, z, xhat, w, b, silu):
+    """How far the fp32 z and y may be from the 64-bit ones."""
+    Bn, S, C = x.shape
+    G = mean.shape[1]
+    n = chain(S, C)
+    aw = 1.0 if w is None else w.double().abs()
+    ab = 0.0 if b is None else b.double().abs()
+    mr = (mean.abs() * rstd)[:, None, :, None].expand(Bn, S, G, C // G).reshape(Bn, S, C)
+    one = 1.0 + xhat.abs()
+    dz = U * (n * (mr + one) * aw + 4 * ab)   # mean off by n U (|mean| + sigma), rstd by n U
+    if not silu:
+        return dz
+    # |y'| <= 1.1; exp is off by 2 + 1.16 |z| steps of 2^-23, the quotient by 4
+    return 1.1 * dz + z.abs() * torch.sigmoid(z) * (6 + 1.2 * z.abs()) * 2 * U
+
+
+NORM_CASES = [
+    # shape [B, ..., C], groups, silu, dtype, parameters, offset
+    ((1, 1, 8), 1, False, torch.bfloat16, "same", 0.0),
+    ((2, 64, 1280), 32, True, torch.bfloat16, "same", 0.0),
+    ((2, 9, 13, 640), 32, True, torch.float16, "float", 1.0),
+    ((3, 257, 24), 3, True, torch.float32, "same", 0.0),
+    ((1, 1000, 320), 32, False, torch.bfloat16, "none", 0.5),       # 10 channels a group
+    ((5, 3, 128), 128, True, torch.bfloat16, "float", 0.0),         # a channel a group
+    ((2, 31, 4096), 32, False, torch.float16, "same", 0.0),
+    ((1, 17, 2048), 1, True, torch.float32, "same", 0.0),
+    ((300, 5, 64), 8, True, torch.bfloat16, "same", 0.0),           # more samples than blocks
+    ((1, 70000, 16), 2, True, torch.bfloat16, "same", 0.0),
+    ((1, 5000, 128), 32, False, torch.float32, "same", 1000.0),     # a mean far from zero
+    ((2, 4, 3, 5, 2, 48), 6, True, torch.float16, "same", 0.0),
+]
+
+
+def make_norm(shape, dtype, params, offset, seed=11):
+    g = gen(seed)
+    C = shape[-1]
+    x = (torch.randn(shape, generator=g) * (0.5 + torch.rand(C, generator=g)) + 0.3 * torch.randn(C, generator=g) + offset).to(dtype)
+    w = b = None
+    if params != "none":
+        pt = torch.float32 if params == "float" else dtype
+        w = (1.0 + 0.3 * torch.randn(C, generator=g)).to(pt)
+        b = (0.3 * torch.randn(C, generator=g)).to(pt)
+    dev = [None if t is None else t.cuda() for t in (x, w, b)]
+    return x, w, b, dev
+
+
+@pytest.mark.parametrize("shape,groups,silu,dtype,params,offset", NORM_CASES)
+def test_group_norm(shape, groups, silu, dtype, params, offset):
+    x, w, b, (xd, wd, bd) = make_norm(shape, dtype, params, offset)
+    y, mean, rstd = w8a8.group_norm(xd, groups, wd, bd, eps=1e-5, activation="silu" if silu else None,
+                                    return_stats=True)
+    x3 = x.view(shape[0], -1, shape[-1])
+    y64, m64, r64, z64, xh64 = norm64(x3, groups, w, b, 1e-5, silu)
+    n = chain(x3.shape[1], shape[-1])
+    close(mean, m64, n * U * (m64.abs() + 1 / r64), "mean")
+    close(rstd, r64, n * U * r64 * (1 + 0 * m64), "rstd")
+    assert y.shape == xd.shape and y.dtype == dtype
+    close(y.view(x3.shape), y64, norm_slack(x3, y64, m64, r64, z64, xh64, w, b, silu), "y")
+    plain = w8a8.group_norm(xd, groups, wd, bd, eps=1e-5, activation="silu" if silu else None)
+    assert torch.equal(plain, y)
+
+
+def test_group_norm_strided_out_and_in_place():
+    x, w, b, (xd, wd, bd) = make_norm((2, 30, 64), torch.bfloat16, "same", 0.0)
+    want = w8a8.group_norm(xd, 8, wd, bd, activation="silu")
+    wide = torch.full((2, 32, 96), 3.0, dtype=torch.bfloat16, device="cuda")
+    src = wide[:, 1:31, 16:80]
+    src.copy_(xd)
+    out = torch.full((2, 33, 80), 5.0, dtype=torch.bfloat16, device="cuda")
+    dst = out[:, 2:32, 8:72]
+    assert torch.equal(w8a8.group_norm(src, 8, wd, bd, activation="silu", out=dst), want)
+    assert (out[:, :2] == 5).all() and (out[:, 32:] == 5).all() and (out[..., :8] == 5).all() and (out[..., 72:] == 5).all()
+    same = xd.clone()
+    w8a8.group_norm(same, 8, wd, bd, activation="silu", out=same)
+    assert torch.equal(same, want)
+
+
+def test_group_norm_takes_channels_last_images():
+    img = torch.randn((2, 32, 6, 7), generator=gen(12)).half().cuda().contiguous(memory_format=torch.channels_last)
+    x = img.permute(0, 2, 3, 1)
+    y = w8a8.group_norm(x, 4)
+    assert torch.equal(y, w8a8.group_norm(x.reshape(2, 42, 32).contiguous(), 4).view(2, 6, 7, 32))
+
+
+def test_group_norm_constant_groups():
+    # no variance: rstd = 1 / sqrt(eps), y = bias
+    x = torch.full((2, 40, 16), 3.0, dtype=torch.bfloat16, device="cuda")
+    w, b = torch.full((16,), 2.0, device="cuda"), torch.arange(16.0, device="cuda")
+    y, mean, rstd = w8a8.group_norm(x, 4, w, b, eps=1e-6, return_stats=True)
+    assert torch.equal(y, b.bfloat16().expand_as(y)) and (mean == 3).all()
+    close(rstd, torch.full((2, 4), 1e3, dtype=torch.float64), torch.tensor(4 * U * 1e3), "rstd")
+
+
+@pytest.mark.parametrize("shape,groups,silu,params", [
+    ((1, 1, 16), 2, False, "same"), ((2, 100, 1280), 32, False, "same"), ((2, 37, 320), 32, True, "float"),
+    ((1, 3000, 48), 6, True, "none"), ((3, 5, 4096), 32, False, "same"), ((1, 130, 2064), 1, True, "same"),
+])
+def test_group_norm_quant(shape, groups, silu, params):
+    x, w, b, (xd, wd, bd) = make_norm(shape, torch.bfloat16, params, 0.2)
+    q, s, mean, rstd = w8a8.group_norm_quant(xd, groups, wd, bd, activation="silu" if silu else None, return_stats=True)
+    y64, m64, r64, z64, xh64 = norm64(x, groups, w, b, 1e-5, silu)
+    slack = norm_slack(x, y64, m64, r64, z64, xh64, w, b, silu).reshape(-1, shape[-1])
+    y64 = y64.view(-1, shape[-1])
+    amax = y64.abs().amax(1)
+    close(s, amax / 127, slack.amax(1) / 127 + 2 * U * amax / 127, "scales")
+    assert q.shape == y64.shape and s.shape == amax.shape
+    qs = q.cpu().double() * s.cpu().double()[:, None]
+    # half a code, and what the quotient's rounding moves
+    tol = s.cpu().double()[:, None] * (0.5 + 127 * 2 * U) + slack
+    assert ((qs - y64).abs() <= tol).all()
+    assert (q.cpu().abs().amax(1) == 127).logical_or(s.cpu() == 0).all()
+    ys, m2, r2 = w8a8.group_norm(xd, groups, wd, bd, activation="silu" if silu else None, return_stats=True)
+    assert torch.equal(m2, mean) and torch.equal(r2, rstd)
+
+
+def test_group_norm_quant_zero_rows():
+    # no variance and no bias: rows of zeros have scale 0 and codes 0
+    x = torch.full((2, 5, 32), -1.5, dtype=torch.bfloat16, device="cuda")
+    q, s = w8a8.group_norm_quant(x, 4)
+    assert (q == 0).all() and (s == 0).all()
+
+
+def grads64(dy, x, G, w, b, mean, rstd, silu):
+    Bn, S, C = x.shape
+    sh = (Bn, S, G, C // G)
+    xh = ((x.double().view(sh) - mean.double()[:, None, :, None]) * rstd.double()[:, None, :, None]).view(Bn, S, C)
+    w64 = torch.ones(C, dtype=torch.float64) if w is None else w.double()
+    z = xh * w64 + (0.0 if b is None else b.double())
+    sig = torch.sigmoid(z)
+    d = sig * (1 + z * (1 - sig)) if silu else torch.ones_like(z)
+    dz = dy.double() * d
+    wdz = (dz * w64).view(sh)
+    xg = xh.view(sh)
+    c1, c2 = wdz.mean((1, 3), keepdim=True), (wdz * xg).mean((1, 3), keepdim=True)
+    r = rstd.double()[:, None, :, None]
+    dx = (r * (wdz - c1 - xg * c2)).view(Bn, S, C)
+    # fp32 slack.  xh: U (|xh| 3 + |mean| rstd); z and the derivative from it
+    # (|y''| <= 0.5), the derivative's own quotient and exponential
+    n = chain(S, C)
+    mr = (mean.double().abs() * rstd.double())[:, None, :, None].expand(sh).reshape(Bn, S, C)
+    exh = U * (3 * xh.abs() + 2 * mr)
+    ez = exh * w64.abs() + 2 * U * z.abs()
+    ed = (0.5 * ez + (8 + 1.2 * z.abs()) * (1 + z.abs()) * 2 * U) if silu else 0 * z
+    edz = dy.double().abs() * ed + 2 * U * dz.abs()
+    adz, axh = dz.abs(), xh.abs()
+    sl_db = (edz + n * U * adz).sum((0, 1))
+    sl_dw = (edz * axh + adz * exh + n * U * adz * axh).sum((0, 1))
+    ew = (edz * w64.abs()).view(sh)
+    awdz = wdz.abs()
+    e1 = (ew + (n + 4) * U * awdz).mean((1, 3), keepdim=True)
+    e2 = (ew * xg.abs() + awdz * exh.view(sh) + (n + 4) * U * awdz * xg.abs()).mean((1, 3), keepdim=True)
+    sl_dx = r * (ew + e1 + xg.abs() * e2 + exh.view(sh) * c2.abs() + 4 * U * (awdz + c1.abs() + (xg * c2).abs()))
+    return (dx, sl_dx.reshape(Bn, S, C)), ((dz * xh).sum((0, 1)), sl_dw), (dz.sum((0, 1)), sl_db)
+
+
+@pytest.mark.parametrize("shape,groups,silu,dtype,params,offset", NORM_CASES)
+def test_group_norm_backward(shape, groups, silu, dtype, params, offset):
+    x, w, b, (xd, wd, bd) = make_norm(shape, dtype, params, offset)
+    act = "silu" if silu else None
+    _, mean, rstd = w8a8.group_norm(xd, groups, wd, bd, activation=act, return_stats=True)
+    dy = torch.randn(shape, generator=gen(13)).to(dtype)
+    dx, dw, db = w8a8.group_norm_backward(dy.cuda(), xd, mean, rstd, wd, bd, activation=act)
+    x3, dy3 = x.view(shape[0], -1, shape[-1]), dy.view(shape[0], -1, shape[-1])
+    wx, ww, wb = grads64(dy3, x3, groups, w, b, mean.cpu(), rstd.cpu(), silu)
+    close(dx.view(x3.shape), wx[0], wx[1], "dx")
+    if w is None:
+        assert dw is None and db is None
+    else:
+        close(dw, *ww, "dweight")
+        close(db, *wb, "dbias")
+    again = w8a8.group_norm_backward(dy.cuda(), xd, mean, rstd, wd, bd, activation=act)
+    assert torch.equal(again[0], dx) and (w is None or (torch.equal(again[1], dw) and torch.equal(again[2], db)))
+    same = dy.cuda()
+    assert torch.equal(w8a8.group_norm_backward(same, xd, mean, rstd, wd, bd, activation=act, out=same)[0], dx)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+def test_group_norm_gradient_against_differences(silu):
+    # the 64-bit forward's central differences along random directions
+    x, w, b, (xd, wd, bd) = make_norm((2, 21, 24), torch.float32, "same", 0.0)
+    act = "silu" if silu else None
+    _, mean, rstd = w8a8.group_norm(xd, 3, wd, bd, activation=act, return_stats=True)
+    dy = torch.randn(x.shape, generator=gen(14))
+    dx, dw, db = w8a8.group_norm_backward(dy.cuda(), xd, mean, rstd, wd, bd, activation=act)
+    f = lambda xx, ww, bb: (norm64(xx, 3, ww, bb, 1e-5, silu)[0] * dy.double()).sum()  # noqa: E731
+    h = 1e-4
+    for i, g in enumerate((dx, dw, db)):
+        args = [x.double(), w.double(), b.double()]
+        v = torch.randn(args[i].shape, generator=gen(15 + i), dtype=torch.float64)
+        plus, minus = list(args), list(args)
+        plus[i], minus[i] = args[i] + h * v, args[i] - h * v
+        diff = (f(*plus) - f(*minus)) / (2 * h)
+        got = (g.cpu().double() * v).sum()
+        # fp32 gradients: some 100 U of every term; third derivatives of order
+        # rstd^3 |dy| |v|^3 leave h^2 of them
+        scale = (g.cpu().double().abs() * v.abs()).sum() + (dy.abs().double().sum() * v.abs().max())
+        assert abs(got - diff) <= scale * (100 * U + 10 * h * h)
+
+
+# ----------------------------------------------------------------- input gradient
+
+def input_grad_ref(dy, Wq, s_w):
+    """The definition, in numpy: fp32 rows and codes, exact sums."""
+    g = dy.float().numpy() * s_w.numpy()
+    s = (np.abs(g).max(1) / np.float32(127)).astype(np.float32)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        c = np.where(s[:, None] > 0, np.clip(np.rint(g / s[:, None]), -127, 127), 0).astype(np.float64)
+    acc = c @ Wq.numpy().astype(np.float64)        # |acc| < 2^31: exact in 64-bit floats
+    y = acc.astype(np.float32) * s[:, None]
+    return torch.from_numpy(y).bfloat16(), torch.from_numpy(c), torch.from_numpy(s)
+
+
+def make_grad(M, N, K, seed):
+    g = gen(seed)
+    dy = (torch.randn((M, N), generator=g) * 1e-3).bfloat16()
+    if M > 2:
+        dy[M // 2] = 0  # a row of zeros
+    Wq = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int8)
+    s_w = (0.5 + torch.rand(N, generator=g)) * 1e-3
+    return dy, Wq, s_w
+
+
+GRAD_SHAPES = [
+    (1, 8, 16), (1, 136, 128), (3, 4096, 4096), (16, 1000, 528), (17, 264, 144), (33, 520, 1040), (64, 256, 128),
+    (129, 2056, 272), (300, 264, 256), (511, 1032, 2064), (700, 4096, 1024), (5, 13000, 256), (260, 24, 16),
+    (1300, 520, 4112),
+]
+
+
+@pytest.mark.parametrize("M,N,K", GRAD_SHAPES)
+def test_linear_input_grad_is_exact(M, N, K):
+    dy, Wq, s_w = make_grad(M, N, K, M + N)
+    want = input_grad_ref(dy, Wq, s_w)[0]
+    got = w8a8.linear_input_grad(dy.cuda(), Wq.cuda(), s_w.cuda())
+    assert got.shape == (M, K)
+    assert torch.equal(got.cpu(), want), f"{int((got.cpu() != want).sum())} of {want.numel()} differ"
+
+
+@pytest.mark.parametrize("variant", [B.VARIANT_GEMM_BN128, B.VARIANT_GEMM_BN256, B.VARIANT_GEMM_PAIR, B.VARIANT_GEMV_TC])
+@pytest.mark.parametrize("M,N,K", [(1, 24, 16), (37, 1000, 528), (128, 392, 2048), (300, 5128, 272), (2600, 264, 2320)])
+def test_linear_input_grad_variants_agree(M, N, K, variant):
+    dy, Wq, s_w = make_grad(M, N, K, 21)
+    if variant == B.VARIANT_GEMV_TC and M > 128:
+        with pytest.raises(w8a8.W8A8Error):
+            w8a8.linear_input_grad(dy.cuda(), Wq.cuda(), s_w.cuda(), variant=variant)
+        return
+    got = w8a8.linear_input_grad(dy.cuda(), Wq.cuda(), s_w.cuda(), variant=variant)
+    assert torch.equal(got.cpu(), input_grad_ref(dy, Wq, s_w)[0])
+
+
+def test_linear_input_grad_strides_and_out():
+    dy, Wq, s_w = make_grad(70, 200, 96, 22)
+    wide = torch.zeros((70, 224), dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:208] = dy.cuda()
+    big = torch.full((72, 112), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = big[1:71, 8:104]
+    w8a8.linear_input_grad(wide[:, 8:208], Wq.cuda(), s_w.cuda(), out=out)
+    assert torch.equal(out.cpu(), input_grad_ref(dy, Wq, s_w)[0])
+    big[1:71, 8:104] = 9.0
+    assert (big == 9).all()
+
+
+def test_linear_input_grad_against_the_unrounded_product():
+    # every code stands within half a step of its value: the product is off by
+    # at most s_g / 2 * sum |Wq| and its own rounding
+    dy, Wq, s_w = make_grad(40, 520, 256, 23)
+    got = w8a8.linear_input_grad(dy.cuda(), Wq.cuda(), s_w.cuda())
+    full = (dy.double() * s_w.double()) @ Wq.double()
+    s = (dy.double() * s_w.double()).abs().amax(1, keepdim=True) / 127
+    slack = s * (0.5 + 127 * 4 * U) * Wq.double().abs().sum(0) + 4 * U * full.abs()
+    close(got, full, slack, "dx")
+    # and against differences of the layer: <dx, v> = d/dh <dy, (x + h v) W^T>
+    v = torch.randn((40, 256), generator=gen(24), dtype=torch.float64)
+    w64 = Wq.double() * s_w.double()[:, None]
+    fwd = lambda x: ((x @ w64.T) * dy.double()).sum()  # noqa: E731
+    diff = (fwd(v) - fwd(-v)) / 2
+    tol = ((slack + rounding(full.abs() + slack, torch.bfloat16)) * v.abs()).sum()
+    assert abs((got.cpu().double() * v).sum() - diff) <= tol
+
+
+# ----------------------------------------------------------------- together
+
+def block(x, p, act_rows):
+    """One attention input: norm -> int8 projection -> rotary on q and k."""
+    q8, s_a, mean, rstd = w8a8.group_norm_quant(x, p["groups"], p["w"], p["b"], return_stats=True)
+    y = w8a8.linear(q8, s_a, p["Wq"], p["s_w"], p["bias"]).view(x.shape[0], act_rows, 3 * p["heads"], p["dim"])
+    H = p["heads"]
+    q, k = w8a8.rotary(y[:, :, :H], p["pos"], p["freq"], k=y[:, :, H:2 * H], out=y[:, :, :H], out_k=y[:, :, H:2 * H])
+    return y, mean, rstd
+
+
+def block_grad(dy, x, mean, rstd, p):
+    H = p["heads"]
+    w8a8.rotary(dy[:, :, :H], p["pos"], p["freq"], k=dy[:, :, H:2 * H], backward=True, out=dy[:, :, :H],
+                out_k=dy[:, :, H:2 * H])
+    dh = w8a8.linear_input_grad(dy.view(-1, 3 * H * p["dim"]), p["Wq"], p["s_w"])
+    return w8a8.group_norm_backward(dh.view(x.shape), x, mean, rstd, p["w"], p["b"])
+
+
+def make_block(Bn, S, C, heads, dim):
+    g = gen(31)
+    x = (torch.randn((Bn, S, C), generator=g) + 0.3).bfloat16().cuda()
+    W = (torch.randn((3 * heads * dim, C), generator=g) * 0.05).bfloat16().cuda()
+    Wq, s_w = w8a8.quantize_weights(W)
+    p = {"groups": 8, "w": (1 + 0.1 * torch.randn(C, generator=g)).bfloat16().cuda(),
+         "b": (0.1 * torch.randn(C, generator=g)).bfloat16().cuda(), "Wq": Wq, "s_w": s_w,
+         "bias": (0.1 * torch.randn(3 * heads * dim, generator=g)).bfloat16().cuda(), "heads": heads, "dim": dim,
+         "pos": torch.arange(S).cuda(), "freq": w8a8.rotary_frequencies(dim)[0]}
+    return x, p
+
+
+@pytest.mark.parametrize("Bn,S,C,heads,dim", [(2, 40, 64, 3, 16), (1, 300, 256, 4, 64)])
+def test_block_forward_and_backward(Bn, S, C, heads, dim):
+    x, p = make_block(Bn, S, C, heads, dim)
+    y, mean, rstd = block(x, p, S)
+    # the same steps in 64 bits, from the device's own int8 rows (their
+    # rounding is checked above)
+    q8, s_a = w8a8.group_norm_quant(x, p["groups"], p["w"], p["b"])
+    lin = (q8.cpu().double() * s_a.cpu().double()[:, None]) @ (p["Wq"].cpu().double() * p["s_w"].cpu().double()[:, None]).T
+    lin = (lin + p["bias"].cpu().double()).view(Bn, S, 3 * heads, dim)
+    # the layer's bf16 result feeds the rotation: each of its values may be
+    # half a bf16 step off (2^-8 of itself)
+    pos = torch.arange(S).expand(Bn, S)[..., None]
+    want, slack = rotary64(lin[:, :, :2 * heads], pos, p["freq"], "interleaved", torch.zeros(dim // 2), 1.0, False)
+    a, b = lin[:, :, :2 * heads, 0::2].abs(), lin[:, :, :2 * heads, 1::2].abs()
+    slack = slack + (2.0 ** -8 + 8 * U) * (a + b).repeat_interleave(2, -1)
+    close(y[:, :, :2 * heads], want, slack, "q and k")
+    close(y[:, :, 2 * heads:], lin[:, :, 2 * heads:], 8 * U * lin[:, :, 2 * heads:].abs(), "v")
+    # backward, step by step against the definitions on the device's own inputs
+    dy = torch.randn(y.shape, generator=gen(32)).bfloat16()
+    turned = dy.cuda()
+    dx, dw, db = block_grad(turned, x, mean, rstd, p)
+    tw, ts = rotary64(dy[:, :, :2 * heads], pos, p["freq"], "interleaved", torch.zeros(dim // 2), 1.0, True)
+    close(turned[:, :, :2 * heads], tw, ts, "turned")
+    dh = input_grad_ref(turned.cpu().reshape(-1, 3 * heads * dim), p["Wq"].cpu(), p["s_w"].cpu())[0].view(x.shape)
+    wx, ww, wb = grads64(dh, x.cpu(), 8, p["w"].cpu(), p["b"].cpu(), mean.cpu(), rstd.cpu(), False)
+    close(dx, *wx, "dx")
+    close(dw, *ww, "dweight")
+    close(db, *wb, "dbias")
+
+
+def test_block_in_a_graph_on_another_stream_and_twice():
+    x, p = make_block(2, 300, 256, 4, 64)
+    dy0 = torch.randn((2, 300, 12, 64), generator=gen(33)).bfloat16().cuda()
+    y_ref, mean, rstd = block(x, p, 300)
+    ref = block_grad(dy0.clone(), x, mean, rstd, p)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    xin, dyin = x.clone(), dy0.clone()
+    with torch.cuda.stream(side):
+        block_grad(dy0.clone(), x, *block(x, p, 300)[1:], p)  # warm up
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y, m, r = block(xin, p, 300)
+        dyc = dyin.clone()
+        dx, dw, db = block_grad(dyc, xin, m, r, p)
+    # other inputs first, then the first ones again: a replay keeps nothing
+    xin.copy_(x.flip(1))
+    dyin.copy_(dy0.flip(2))
+    graph.replay()
+    torch.cuda.synchronize()
+    other = (y.clone(), dx.clone())
+    xin.copy_(x)
+    dyin.copy_(dy0)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, y_ref)
+    for a, b in zip((dx, dw, db), ref):
+        assert torch.equal(a, b)
+    yo, mo, ro = block(x.flip(1).contiguous(), p, 300)
+    assert torch.equal(other[0], yo)
+    assert torch.equal(other[1], block_grad(dy0.flip(2).contiguous(), x.flip(1).contiguous(), mo, ro, p)[0])
+
+
+def test_operators_on_a_given_stream():
+    x, p = make_block(1, 64, 128, 2, 32)
+    y_ref = block(x, p, 64)[0]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    q8, s_a = w8a8.group_norm_quant(x, 8, p["w"], p["b"], stream=s)
+    y = w8a8.linear(q8, s_a, p["Wq"], p["s_w"], p["bias"], stream=s).view(1, 64, 6, 32)
+    q = w8a8.rotary(y[:, :, :4], p["pos"], p["freq"], stream=s)
+    s.synchronize()
+    assert torch.equal(q, y_ref[:, :, :4]) and torch.equal(y[:, :, 4:], y_ref[:, :, 4:])

@@ -9,7 +9,9 @@ dequantization/bias epilogue producing bf16.  The kernels live in
 from .binding import (  # noqa: F401
     LIB_PATH, VARIANT_AUTO, VARIANT_GEMM_BN64, VARIANT_GEMM_BN128, VARIANT_GEMM_BN256,
     VARIANT_GEMM_PAIR, VARIANT_GEMV, VARIANT_GEMV_TC,
-    W8A8Error, last_device_error, lib, linear, linear_fused, linear_fused_host, quant_act,
-    quantize_weights, select, selftest_bounded_wait, status_string, unpack_int32_weights, version,
-    w8a16_linear, workspace_size,
+    W8A8Error, group_norm, group_norm_backward, group_norm_quant, group_norm_workspace_size,
+    input_grad_workspace_size, last_device_error, lib, linear, linear_fused, linear_fused_host,
+    linear_input_grad, quant_act, quantize_weights, rotary, rotary_frequencies, select,
+    selftest_bounded_wait, status_string, unpack_int32_weights, version, w8a16_linear,
+    workspace_size,
 )

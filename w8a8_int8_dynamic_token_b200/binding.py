@@ -15,6 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import math
 import os
 import re
 
@@ -44,6 +45,14 @@ VARIANT_NAMES = {0: "auto", 1: "gemv", 2: "gemm_bn128", 3: "gemm_bn256", 4: "gem
                  5: "gemm_bn64", 6: "gemv_tc"}
 
 
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
+ROTARY_INTERLEAVED, ROTARY_HALF = 0, 1
+ACT_NONE, ACT_SILU = 0, 1
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
+_LAYOUTS = {"interleaved": ROTARY_INTERLEAVED, "half": ROTARY_HALF}
+_ACTIVATIONS = {None: ACT_NONE, "silu": ACT_SILU}
+
+
 class W8A8Error(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -62,9 +71,17 @@ class Plan(ctypes.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
 
+class RotaryHeads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("x_batch", ctypes.c_int64), ("x_token", ctypes.c_int64),
+                ("x_head", ctypes.c_int64), ("y_batch", ctypes.c_int64),
+                ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64)]
+
+
 _lib = None
 _vp, _i64, _i32, _int, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int,
                               ctypes.c_size_t)
+_f32 = ctypes.c_float
 
 _SIGNATURES = {
     "w8a8_status_string": ([_int], ctypes.c_char_p),
@@ -87,6 +104,20 @@ _SIGNATURES = {
     "w8a8_linear_fused_noalloc": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp],
                                   _int),
     "w8a16_linear": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp], _int),
+    "w8a8_input_grad_workspace_size": ([_i64, _i64, _i64, _int, ctypes.POINTER(_sz)], _int),
+    "w8a8_linear_input_grad": ([_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _int, _vp, _sz,
+                                _vp], _int),
+    "w8a8_rotary": ([ctypes.POINTER(RotaryHeads), _int, _int, _i64, _i64, _i64, _i64, _int, _vp,
+                     _int, _i64, _i64, _i64, _vp, _vp, _f32, _int, _vp], _int),
+    "w8a8_group_norm_workspace_size": ([_i64, _i64, _i64, _i64, _int, _int, ctypes.POINTER(_sz)],
+                                       _int),
+    "w8a8_group_norm": ([_vp, _i64, _i64, _int, _i64, _i64, _i64, _i64, _vp, _vp, _int, _f32,
+                         _int, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp], _int),
+    "w8a8_group_norm_quant": ([_vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _int, _f32, _int,
+                               _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
+    "w8a8_group_norm_backward": ([_vp, _i64, _i64, _vp, _i64, _i64, _int, _i64, _i64, _i64, _i64,
+                                  _vp, _vp, _vp, _vp, _int, _int, _vp, _i64, _i64, _vp, _vp, _vp,
+                                  _sz, _vp], _int),
     "w8a8_select": ([_i64, _i64, _i64, _i32, _int, ctypes.POINTER(Plan)], _int),
     "w8a8_last_device_error": ([_vp], _int),
     "w8a8_selftest_bounded_wait": ([_i64, _vp], _int),
@@ -198,6 +229,56 @@ def w8a8_linear_fused_noalloc(x, M, K, ldx, Wq, s_w, bias, N, y, ldy, stream) ->
 
 def w8a16_linear_raw(x, M, K, ldx, Wq, s_w, bias, N, y, ldy, stream) -> int:
     return lib().w8a16_linear(x, M, K, ldx, Wq, s_w, bias, N, y, ldy, stream)
+
+
+def w8a8_input_grad_workspace_size(M, N, K, variant) -> tuple[int, int]:
+    out = ctypes.c_size_t(0)
+    st = lib().w8a8_input_grad_workspace_size(M, N, K, variant, ctypes.byref(out))
+    return st, int(out.value)
+
+
+def w8a8_linear_input_grad(dy, M, N, lddy, Wq, s_w, K, dx, lddx, variant, workspace, ws_bytes,
+                           stream) -> int:
+    return lib().w8a8_linear_input_grad(dy, M, N, lddy, Wq, s_w, K, dx, lddx, variant, workspace,
+                                        ws_bytes, stream)
+
+
+def w8a8_rotary(tensors, num_tensors, dtype, batch, tokens, dim, rot, layout, positions,
+                position_bits, pos_batch, pos_token, axes, inv_freq, axis, scale, backward,
+                stream) -> int:
+    return lib().w8a8_rotary(tensors, num_tensors, dtype, batch, tokens, dim, rot, layout,
+                             positions, position_bits, pos_batch, pos_token, axes, inv_freq, axis,
+                             scale, backward, stream)
+
+
+def w8a8_group_norm_workspace_size(B, S, C, G, dtype, backward) -> tuple[int, int]:
+    out = ctypes.c_size_t(0)
+    st = lib().w8a8_group_norm_workspace_size(B, S, C, G, dtype, backward, ctypes.byref(out))
+    return st, int(out.value)
+
+
+def w8a8_group_norm(x, x_batch, x_pixel, dtype, B, S, C, G, weight, bias, param_dtype, eps,
+                    activation, y, y_batch, y_pixel, mean, rstd, workspace, ws_bytes,
+                    stream) -> int:
+    return lib().w8a8_group_norm(x, x_batch, x_pixel, dtype, B, S, C, G, weight, bias, param_dtype,
+                                 eps, activation, y, y_batch, y_pixel, mean, rstd, workspace,
+                                 ws_bytes, stream)
+
+
+def w8a8_group_norm_quant(x, x_batch, x_pixel, B, S, C, G, weight, bias, param_dtype, eps,
+                          activation, q, s_a, mean, rstd, workspace, ws_bytes, stream) -> int:
+    return lib().w8a8_group_norm_quant(x, x_batch, x_pixel, B, S, C, G, weight, bias, param_dtype,
+                                       eps, activation, q, s_a, mean, rstd, workspace, ws_bytes,
+                                       stream)
+
+
+def w8a8_group_norm_backward(dy, dy_batch, dy_pixel, x, x_batch, x_pixel, dtype, B, S, C, G, mean,
+                             rstd, weight, bias, param_dtype, activation, dx, dx_batch, dx_pixel,
+                             dweight, dbias, workspace, ws_bytes, stream) -> int:
+    return lib().w8a8_group_norm_backward(dy, dy_batch, dy_pixel, x, x_batch, x_pixel, dtype, B, S,
+                                          C, G, mean, rstd, weight, bias, param_dtype, activation,
+                                          dx, dx_batch, dx_pixel, dweight, dbias, workspace,
+                                          ws_bytes, stream)
 
 
 def w8a8_select(M, N, K, num_sms=148, variant=VARIANT_AUTO) -> tuple[int, Plan]:
@@ -479,6 +560,327 @@ def linear_fused_host(x_host, Wq, s_w, bias, y_host, x_dev, y_dev, workspace, st
                                       _ptr(y_host), _ptr(x_dev), _ptr(y_dev), _ptr(workspace),
                                       ws_bytes, _stream(s)), "w8a8_linear_fused_host")
     return y_host
+
+
+@functools.lru_cache(maxsize=1024)
+def input_grad_workspace_size(M: int, N: int, K: int, variant: int = VARIANT_AUTO) -> int:
+    st, n = w8a8_input_grad_workspace_size(M, N, K, variant)
+    _check(st, "w8a8_input_grad_workspace_size")
+    return n
+
+
+def _scratch(need, workspace, dev):
+    """(tensor, pointer, bytes) of the caller's workspace, or of a fresh one of
+    `need` bytes (allocated on the launching stream, inside _launching; kept
+    alive by the caller until the launches have been enqueued)."""
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def linear_input_grad(dy, Wq, s_w, out=None, workspace=None, variant=VARIANT_AUTO, stream=None):
+    """Gradient of the layer with respect to its input, through the frozen int8
+    weights: dx [M, K] from dy bf16 [M, N].  The rows dy * s_w are quantized per
+    token and multiplied with Wq as it is stored (exact int32 sums)."""
+    _need(dy, "dy", torch.bfloat16, 2)
+    _need(Wq, "Wq", torch.int8, 2)
+    _need(s_w, "s_w", torch.float32, 1)
+    M, N = dy.shape
+    K = Wq.shape[1]
+    if Wq.shape[0] != N or s_w.shape[0] != N or not Wq.is_contiguous():
+        raise ValueError("shape mismatch between dy, Wq, s_w")
+    if out is not None:
+        _need(out, "out", torch.bfloat16, 2)
+        _shape(out, "out", (M, K))
+    dev = _on_one_device(dy=dy, Wq=Wq, s_w=s_w, out=out, workspace=workspace)
+    need = input_grad_workspace_size(M, N, K, variant)
+    with _launching(dev, stream) as s:
+        dx = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
+        _check(w8a8_linear_input_grad(_ptr(dy), M, N, dy.stride(0), _ptr(Wq), _ptr(s_w), K,
+                                      _ptr(dx), dx.stride(0), variant, ws_ptr, ws_bytes,
+                                      _stream(s)), "w8a8_linear_input_grad")
+        del ws
+    return dx
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None,
+                       factor: float = 1.0, trained: int = 0, fast: float = 32.0,
+                       slow: float = 1.0):
+    """(inv_freq, scale) for rotary(): radians per position of the rot / 2 pairs
+    (CPU float64), f_i = base^(-2i / rot), and the factor on rotated values.
+
+    scaling, for contexts `factor` times the trained one:
+      None       as they are;
+      "linear"   every frequency divided by factor;
+      "base"     base raised to base * factor^(rot / (rot - 2)), which divides
+                 the slowest frequency by factor and keeps the fastest;
+      "ramp"     pairs that turn more than `fast` times over the `trained`
+                 positions are kept, those that turn less than `slow` times are
+                 divided by factor, a linear ramp over the pair index between;
+                 scale = 0.1 ln(factor) + 1.
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and at least 2")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    if scaling == "base":
+        if rot == 2:
+            raise ValueError("scaling 'base' needs rot of at least 4")
+        base = base * factor ** (rot / (rot - 2))
+    freq = torch.pow(torch.tensor(base, dtype=torch.float64), -2.0 * i / rot)
+    if scaling in (None, "base"):
+        return freq, 1.0
+    if scaling == "linear":
+        return freq / factor, 1.0
+    if scaling != "ramp":
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if trained < 1 or not fast > slow > 0.0:
+        raise ValueError("scaling 'ramp' needs trained >= 1 and fast > slow > 0")
+    # the pair that turns t times over the trained positions
+    low, high = (rot * math.log(trained / (t * 2.0 * math.pi)) / (2.0 * math.log(base))
+                 for t in (fast, slow))
+    low, high = max(math.floor(low), 0), min(math.ceil(high), rot // 2 - 1)
+    ramp = ((i - low) / max(high - low, 0.001)).clamp(0.0, 1.0)
+    return freq * (1.0 - ramp) + freq / factor * ramp, 0.1 * math.log(factor) + 1.0
+
+
+def _heads(t, name, dtype):
+    """[tokens, heads, dim] or [batch, tokens, heads, dim]."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+
+
+def _rotary_heads(entry, x, y):
+    four = x.dim() == 4
+    xs, ys = x.stride(), y.stride()
+    entry.x, entry.y, entry.heads = x.data_ptr(), y.data_ptr(), x.shape[-2]
+    entry.x_batch, entry.y_batch = (xs[0], ys[0]) if four else (0, 0)
+    entry.x_token, entry.x_head = xs[-3], xs[-2]
+    entry.y_token, entry.y_head = ys[-3], ys[-2]
+
+
+def rotary(x, positions, inv_freq, k=None, layout="interleaved", axis=None, scale=1.0,
+           backward=False, out=None, out_k=None, stream=None):
+    """Rotary positions on heads x [tokens, heads, dim] or [batch, tokens, heads,
+    dim] (and, in the same launch, on k with its own number of heads); bf16,
+    fp16 or fp32, any strides outside a head.  inv_freq: CPU float64 [rot / 2]
+    radians per position (see rotary_frequencies); the first rot values of a
+    head turn, the others are copied.  positions: int32 or int64 on x's device,
+    [tokens] or [batch, tokens], or with a last dimension of axes when `axis`
+    (CPU int32 [rot / 2], the axis of each pair) is given.  backward=True: the
+    gradient.  out / out_k: where to write; x / k themselves, or memory that
+    does not overlap them.  Returns y, or (y, y_k) with k."""
+    _heads(x, "x", None)
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or \
+            inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a dense 1-D CPU float64 tensor")
+    rot, dim = 2 * inv_freq.shape[0], x.shape[-1]
+    if rot > dim:
+        raise ValueError(f"inv_freq turns {rot} values of a head, which has {dim}")
+    if out is not None:
+        _heads(out, "out", x.dtype)
+        _shape(out, "out", x.shape)
+    if k is not None:
+        _heads(k, "k", x.dtype)
+        if k.dim() != x.dim() or k.shape[:-2] != x.shape[:-2] or k.shape[-1] != dim:
+            raise ValueError("x and k differ in more than their heads")
+        if out_k is not None:
+            _heads(out_k, "out_k", x.dtype)
+            _shape(out_k, "out_k", k.shape)
+    elif out_k is not None:
+        raise ValueError("out_k is given without k")
+    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be an int32 or int64 tensor")
+    batch, tokens = (x.shape[0] if x.dim() == 4 else 1), x.shape[-3]
+    lead = positions.dim()
+    axes = 1
+    if axis is not None:
+        if not isinstance(axis, torch.Tensor) or axis.dtype != torch.int32 or axis.is_cuda or \
+                tuple(axis.shape) != tuple(inv_freq.shape) or not axis.is_contiguous():
+            raise TypeError("axis must be a dense CPU int32 tensor of inv_freq's shape")
+        lead -= 1
+        if lead not in (1, 2):
+            raise ValueError("positions must end in a dimension of axes when axis is given")
+        axes = positions.shape[-1]
+        if axes > 1 and positions.stride(-1) != 1:
+            raise ValueError("positions must have unit stride in its last dimension")
+    if lead not in (1, 2) or positions.shape[lead - 1] != tokens or \
+            (lead == 2 and positions.shape[0] != batch):
+        raise ValueError(f"positions must be [{tokens}] or [{batch}, {tokens}]"
+                         + (" and axes" if axis is not None else ""))
+    dev = _on_one_device(x=x, k=k, positions=positions, out=out, out_k=out_k)
+    ps = positions.stride()
+    with _launching(dev, stream) as s:
+        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+        entries = (RotaryHeads * 2)()
+        _rotary_heads(entries[0], x, y)
+        y_k = None
+        if k is not None:
+            y_k = out_k if out_k is not None else torch.empty(k.shape, dtype=x.dtype, device=dev)
+            _rotary_heads(entries[1], k, y_k)
+        _check(w8a8_rotary(entries, 1 if k is None else 2, _DTYPES[x.dtype], batch, tokens, dim, rot,
+                           _LAYOUTS[layout], positions.data_ptr(), 8 * positions.element_size(),
+                           ps[0] if lead == 2 else 0, ps[lead - 1], axes, inv_freq.data_ptr(),
+                           None if axis is None else axis.data_ptr(), scale, int(bool(backward)),
+                           _stream(s)), "w8a8_rotary")
+    return y if k is None else (y, y_k)
+
+
+@functools.lru_cache(maxsize=1024)
+def group_norm_workspace_size(B: int, S: int, C: int, groups: int, dtype=torch.bfloat16,
+                              backward: bool = False) -> int:
+    st, n = w8a8_group_norm_workspace_size(B, S, C, groups, _DTYPES[dtype], int(backward))
+    _check(st, "w8a8_group_norm_workspace_size")
+    return n
+
+
+def _pixels(t, name, shape=None, dtype=None):
+    """Channels-last [B, ..., C]: (B, pixels, C, sample stride, pixel stride).
+    The dimensions between must be evenly strided, as one run of pixels."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
+    if t.dim() < 3:
+        raise ValueError(f"{name} must be [B, ..., C] with its channels last")
+    if shape is not None:
+        _shape(t, name, shape)
+    sizes, strides = t.shape, t.stride()
+    if sizes[-1] > 1 and strides[-1] != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    if t.dim() == 3:
+        return sizes[0], sizes[1], sizes[2], strides[0], strides[1]
+    pixels, step = 1, 0
+    for n, st in zip(reversed(sizes[1:-1]), reversed(strides[1:-1])):
+        if n == 1:
+            continue
+        if pixels == 1:
+            step = st
+        elif st != step * pixels:
+            raise ValueError(f"{name}'s pixels must be evenly strided")
+        pixels *= n
+    return sizes[0], pixels, sizes[-1], strides[0], step or sizes[-1]
+
+
+def _norm_params(x, C, weight, bias):
+    """The type code of weight and bias ([C], both in x's type or in fp32)."""
+    dtype = x.dtype
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype not in (x.dtype, torch.float32):
+            raise TypeError(f"{name} must be a {x.dtype} or float32 tensor")
+        if tuple(t.shape) != (C,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a dense [{C}] tensor")
+        dtype = t.dtype
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same type")
+    return _DTYPES[dtype]
+
+
+def _activation(activation):
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+    return _ACTIVATIONS[activation]
+
+
+def group_norm(x, groups, weight=None, bias=None, eps=1e-5, activation=None, out=None,
+               return_stats=False, workspace=None, stream=None):
+    """Group normalization of a channels-last x [B, ..., C] (bf16, fp16, fp32)
+    with an optional SiLU: y in x's type and shape (and, with return_stats, the
+    mean and 1 / standard deviation, fp32 [B, groups], that the backward pass
+    takes).  out may be x itself."""
+    B, S, C, xb, xs = _pixels(x, "x")
+    act = _activation(activation)
+    pdt = _norm_params(x, C, weight, bias)
+    if out is not None:
+        _, _, _, yb, ys = _pixels(out, "out", x.shape, x.dtype)
+    dev = _on_one_device(x=x, weight=weight, bias=bias, out=out, workspace=workspace)
+    need = group_norm_workspace_size(B, S, C, groups, x.dtype)
+    with _launching(dev, stream) as s:
+        y = out
+        if y is None:
+            y, yb, ys = torch.empty(x.shape, dtype=x.dtype, device=dev), S * C, C
+        mean = rstd = None
+        if return_stats:
+            mean, rstd = torch.empty((2, B, groups), dtype=torch.float32, device=dev).unbind()
+        ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
+        _check(w8a8_group_norm(_ptr(x), xb, xs, _DTYPES[x.dtype], B, S, C, groups, _ptr(weight),
+                               _ptr(bias), pdt, eps, act, _ptr(y), yb, ys, _ptr(mean), _ptr(rstd),
+                               ws_ptr, ws_bytes, _stream(s)), "w8a8_group_norm")
+        del ws
+    return (y, mean, rstd) if return_stats else y
+
+
+def group_norm_quant(x, groups, weight=None, bias=None, eps=1e-5, activation=None,
+                     return_stats=False, workspace=None, stream=None):
+    """group_norm of a bf16 x as the operand of linear(): (q int8 [B * pixels,
+    C], s_a fp32 [B * pixels]), the rows of the fp32 result quantized per pixel
+    (and the statistics, with return_stats)."""
+    B, S, C, xb, xs = _pixels(x, "x", None, torch.bfloat16)
+    act = _activation(activation)
+    pdt = _norm_params(x, C, weight, bias)
+    dev = _on_one_device(x=x, weight=weight, bias=bias, workspace=workspace)
+    need = group_norm_workspace_size(B, S, C, groups, x.dtype)
+    with _launching(dev, stream) as s:
+        q = torch.empty((B * S, C), dtype=torch.int8, device=dev)
+        s_a = torch.empty((B * S,), dtype=torch.float32, device=dev)
+        mean = rstd = None
+        if return_stats:
+            mean, rstd = torch.empty((2, B, groups), dtype=torch.float32, device=dev).unbind()
+        ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
+        _check(w8a8_group_norm_quant(_ptr(x), xb, xs, B, S, C, groups, _ptr(weight), _ptr(bias),
+                                     pdt, eps, act, _ptr(q), _ptr(s_a), _ptr(mean), _ptr(rstd),
+                                     ws_ptr, ws_bytes, _stream(s)), "w8a8_group_norm_quant")
+        del ws
+    return (q, s_a, mean, rstd) if return_stats else (q, s_a)
+
+
+def group_norm_backward(dy, x, mean, rstd, weight=None, bias=None, activation=None, out=None,
+                        workspace=None, stream=None):
+    """Gradients of group_norm (or, straight through the rounding, of
+    group_norm_quant): (dx in x's type, dweight, dbias fp32 [C], None where
+    there is no such parameter).  mean, rstd: the forward's statistics; out may
+    be dy or x itself."""
+    B, S, C, xb, xs = _pixels(x, "x")
+    _, _, _, gb, gs = _pixels(dy, "dy", x.shape, x.dtype)
+    act = _activation(activation)
+    pdt = _norm_params(x, C, weight, bias)
+    _need(mean, "mean", torch.float32, 2)
+    groups = mean.shape[1]
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _need(t, name, torch.float32, 2)
+        _shape(t, name, (B, groups))
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be dense")
+    if out is not None:
+        _, _, _, ob, os_ = _pixels(out, "out", x.shape, x.dtype)
+    dev = _on_one_device(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, bias=bias, out=out,
+                         workspace=workspace)
+    need = group_norm_workspace_size(B, S, C, groups, x.dtype, True)
+    with _launching(dev, stream) as s:
+        dx = out
+        if dx is None:
+            dx, ob, os_ = torch.empty(x.shape, dtype=x.dtype, device=dev), S * C, C
+        dweight = None if weight is None else torch.empty((C,), dtype=torch.float32, device=dev)
+        dbias = None if bias is None else torch.empty((C,), dtype=torch.float32, device=dev)
+        ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
+        _check(w8a8_group_norm_backward(_ptr(dy), gb, gs, _ptr(x), xb, xs, _DTYPES[x.dtype], B, S, C,
+                                        groups, _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias),
+                                        pdt, act, _ptr(dx), ob, os_, _ptr(dweight), _ptr(dbias),
+                                        ws_ptr, ws_bytes, _stream(s)), "w8a8_group_norm_backward")
+        del ws
+    return dx, dweight, dbias
 
 
 def last_device_error(stream=None) -> int:

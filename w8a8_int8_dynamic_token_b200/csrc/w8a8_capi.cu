@@ -8,6 +8,7 @@
 
 #include <atomic>
 #include <chrono>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -16,11 +17,14 @@
 #include "../../include/w8a8.h"
 #include "w8a8_gemm.cuh"
 #include "w8a8_gemv.cuh"
+#include "w8a8_input_grad.cuh"
+#include "w8a8_norm.cuh"
 #include "w8a8_pack.cuh"
 #include "w8a8_peak.cuh"
 #include "w8a16_tmem.cuh"
 #include "w8a8_ptx.cuh"
 #include "w8a8_quant.cuh"
+#include "w8a8_rotary.cuh"
 #include "w8a8_swapab.cuh"
 
 namespace w8a8 {
@@ -520,6 +524,27 @@ int encode_i8_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, i
   return W8A8_OK;
 }
 
+// int8 matrix [rows, cols] whose rows are ld bytes apart (a multiple of 16),
+// box = 128 x box_rows, 128-byte swizzle; columns past cols read as zero (the
+// input gradient's codes).
+int encode_i8_ld_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld,
+                     int box_rows) {
+  const MapKey key{5, base, rows, cols, ld, box_rows};
+  if (map_lookup(key, map)) return W8A8_OK;
+  PFN_cuTensorMapEncodeTiled_v12000 enc = get_encoder();
+  if (enc == nullptr) return W8A8_ERR_CUDA;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims,
+                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return W8A8_ERR_CUDA;
+  map_store(key, *map);
+  return W8A8_OK;
+}
+
 // bf16 matrix [rows, cols] with row stride ld elements, box 64 (cols) x
 // box_rows, 128-byte swizzle (the W8A16 GEMM's activation operand).
 int encode_bf16_load_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols,
@@ -919,6 +944,296 @@ int launch_swapab(const w8a8_plan &plan, const int8_t *q, const float *s_a, int6
     case 64: return launch_swapab_t<64, RAW>(plan, q, s_a, M, K, wq, s_w, bias, N, y, ldy, acc, stream);
     default: return launch_swapab_t<128, RAW>(plan, q, s_a, M, K, wq, s_w, bias, N, y, ldy, acc, stream);
   }
+}
+
+// ---------------------------------------------------------------- input gradient
+
+// Plan of the input gradient: rows M, output columns K, contraction N.  The
+// layer's plan for a [K, N] weight, without the variants that have no
+// MN-major form: the GEMV goes to the tensor-core small-M kernel, the
+// 64-column tiles to 128.
+int select_input_grad_plan(int64_t M, int64_t N, int64_t K, int32_t sms, int variant, int max_smem,
+                           w8a8_plan *plan) {
+  if (variant == W8A8_VARIANT_GEMV || variant == W8A8_VARIANT_GEMM_BN64)
+    return W8A8_ERR_UNSUPPORTED_SHAPE;
+  int st = select_plan(M, K, N, sms, variant, max_smem, plan);
+  if (st != W8A8_OK || variant != W8A8_VARIANT_AUTO) return st;
+  if (plan->variant == W8A8_VARIANT_GEMV)
+    return select_plan(M, K, N, sms, W8A8_VARIANT_GEMV_TC, max_smem, plan);
+  if (plan->variant == W8A8_VARIANT_GEMM_BN64)
+    return select_plan(M, K, N, sms, W8A8_VARIANT_GEMM_BN128, max_smem, plan);
+  return W8A8_OK;
+}
+
+// Bytes between the codes' rows (16-byte rows for the TMA loads).
+inline int64_t grad_code_stride(int64_t N) { return cdiv(N, 16) * 16; }
+
+// Codes and row scales, ahead of the K-split region.
+size_t input_grad_head_bytes(int64_t M, int64_t N) {
+  return align256(static_cast<size_t>(M) * static_cast<size_t>(grad_code_stride(N))) +
+         align256(static_cast<size_t>(M) * sizeof(float));
+}
+
+int launch_quant_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, const float *s_w,
+                      int8_t *codes, float *s_g, cudaStream_t stream) {
+  const uint16_t *src = static_cast<const uint16_t *>(dy);
+  const int64_t ldc = grad_code_stride(N);
+  const dim3 grid(static_cast<unsigned>(M));
+  const int n32 = static_cast<int>(N);
+  switch (cdiv(N / 8, 256)) {
+    case 1: return launch_ex(true, quant_grad_rows_kernel<1>, grid, dim3(256), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
+    case 2: return launch_ex(true, quant_grad_rows_kernel<2>, grid, dim3(256), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
+    case 3: case 4: return launch_ex(true, quant_grad_rows_kernel<4>, grid, dim3(256), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
+    case 5: case 6: return launch_ex(true, quant_grad_rows_kernel<6>, grid, dim3(256), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
+    default: return launch_ex(true, quant_grad_rows_kernel<0>, grid, dim3(256), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
+  }
+}
+
+template <int BN, int STAGES>
+int launch_input_grad_gemm(const w8a8_plan &plan, const int8_t *codes, const float *s_g, int64_t M,
+                           int64_t N, const int8_t *wq, int64_t K, void *dx, int64_t lddx,
+                           cudaStream_t stream) {
+  using L = GemmLayout<BN, STAGES>;
+  CUtensorMap ma, mb, my;
+  int st = encode_i8_ld_map(&ma, codes, M, N, grad_code_stride(N), kBM);
+  if (st != W8A8_OK) return st;
+  st = encode_i8_map(&mb, wq, N, K, kBK);
+  if (st != W8A8_OK) return st;
+  st = encode_bf16_store_map(&my, dx, M, K, lddx);
+  if (st != W8A8_OK) return st;
+  GemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.M = static_cast<int32_t>(M);
+  p.N = static_cast<int32_t>(K);
+  p.K = static_cast<int32_t>(N);
+  p.num_m_blk = static_cast<int32_t>(cdiv(M, kBM));
+  p.num_n_blk = static_cast<int32_t>(cdiv(K, BN));
+  p.num_tiles = plan.num_tiles;
+  p.k_blocks = static_cast<int32_t>(cdiv(N, kBK));
+  p.group_m = kGemmGroupM;
+  p.s_a = s_g;
+  p.y = static_cast<uint16_t *>(dx);
+  p.ldy = lddx;
+  constexpr auto kernel = gemm_i8_tcgen05_kernel<BN, STAGES, false, true>;
+  st = ensure_smem_limit<kernel>(L::kSmemBytes);
+  if (st != W8A8_OK) return st;
+  return launch_ex(true, kernel, dim3(plan.grid), dim3(kGemmThreads), L::kSmemBytes, stream, ma,
+                   mb, my, p);
+}
+
+int launch_input_grad_pair(const w8a8_plan &plan, const int8_t *codes, const float *s_g, int64_t M,
+                           int64_t N, const int8_t *wq, int64_t K, void *dx, int64_t lddx,
+                           const SplitRegion &split, cudaStream_t stream) {
+  using L = PairLayout<kGemmStagesPair>;
+  CUtensorMap ma, mb, my;
+  int st = encode_i8_ld_map(&ma, codes, M, N, grad_code_stride(N), kBM);
+  if (st != W8A8_OK) return st;
+  st = encode_i8_map(&mb, wq, N, K, kBK);
+  if (st != W8A8_OK) return st;
+  st = encode_bf16_store_map(&my, dx, M, K, lddx);
+  if (st != W8A8_OK) return st;
+  GemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.M = static_cast<int32_t>(M);
+  p.N = static_cast<int32_t>(K);
+  p.K = static_cast<int32_t>(N);
+  p.num_m_blk = static_cast<int32_t>(cdiv(M, 256));
+  p.num_n_blk = static_cast<int32_t>(cdiv(K, kPairBN));
+  p.num_tiles = plan.num_tiles;
+  p.k_blocks = static_cast<int32_t>(cdiv(N, kBK));
+  p.group_m = kGemmGroupM / 2;
+  p.s_a = s_g;
+  p.y = static_cast<uint16_t *>(dx);
+  p.ldy = lddx;
+  p.dp_tiles = plan.num_tiles;
+  p.tail_nsplit = 1;
+  int grid = plan.grid;
+  if (plan.tail_tiles_nsplit > 1) {
+    p.tail_nsplit = plan.tail_tiles_nsplit;
+    p.dp_tiles = plan.num_tiles - plan.num_tiles % (plan.grid / 2);
+  } else if (plan.split_tiles > 0 && split.counters != nullptr) {
+    p.dp_tiles = plan.num_tiles - plan.split_tiles;
+    p.sk_per = plan.split_kblocks_per_pair;
+    p.sk_units = plan.split_tiles * p.k_blocks;
+    p.split_partials = split.partials;
+    p.split_counters = split.counters;
+    p.split_epoch = next_tag(56);
+  } else if (plan.split_tiles > 0 && plan.num_tiles < plan.grid / 2) {
+    grid = 2 * plan.num_tiles;  // unsplit and under one wave: one pair per tile
+  }
+  constexpr auto kernel = gemm_i8_tcgen05_pair_kernel<kGemmStagesPair, false, false, true>;
+  st = ensure_smem_limit<kernel>(L::kSmemBytes);
+  if (st != W8A8_OK) return st;
+  return launch_ex(true, kernel, dim3(grid), dim3(kGemmThreads), L::kSmemBytes, stream, ma, mb,
+                   mb, my, p);
+}
+
+template <int MPAD>
+int launch_input_grad_swap(const w8a8_plan &plan, const int8_t *codes, const float *s_g, int64_t M,
+                           int64_t N, const int8_t *wq, int64_t K, void *dx, int64_t lddx,
+                           cudaStream_t stream) {
+  using L = SwapLayout<MPAD>;
+  CUtensorMap mw, mq;
+  int st = encode_i8_map(&mw, wq, N, K, kBK);
+  if (st != W8A8_OK) return st;
+  st = encode_i8_ld_map(&mq, codes, M, N, grad_code_stride(N), MPAD);
+  if (st != W8A8_OK) return st;
+  SwapParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.M = static_cast<int32_t>(M);
+  p.N = static_cast<int32_t>(K);
+  p.K = static_cast<int32_t>(N);
+  p.k_blocks = static_cast<int32_t>(cdiv(N, kBK));
+  p.split = plan.k_split;
+  p.s_a = s_g;
+  p.y = static_cast<uint16_t *>(dx);
+  p.ldy = lddx;
+  constexpr auto kernel = gemm_i8_swapab_kernel<MPAD, false, true>;
+  st = ensure_smem_limit<kernel>(L::kSmemBytes);
+  if (st != W8A8_OK) return st;
+  return launch_cl(true, static_cast<unsigned>(plan.k_split), kernel, dim3(plan.grid),
+                   dim3(kSwThreads), L::kSmemBytes, stream, mw, mq, p);
+}
+
+// ---------------------------------------------------------------- rotary positions
+
+inline int dtype_size(int dtype) { return dtype == W8A8_DTYPE_FP32 ? 4 : 2; }
+
+// Turns per position * 2^64 of a frequency in radians per position.
+unsigned long long turns_q64(double radians) {
+  double t = radians / 6.283185307179586476925286766559;
+  t -= std::floor(t);
+  const double v = std::ldexp(t, 64);
+  return v >= 18446744073709551616.0 ? 0ull : static_cast<unsigned long long>(v);
+}
+
+// Whether rows that start at p and lie `strides` apart allow 16-byte accesses.
+bool wide_rows(const void *p, int64_t sb, int64_t st, int64_t sh, int vec) {
+  return aligned16(p) && sb % vec == 0 && st % vec == 0 && sh % vec == 0;
+}
+
+template <typename T, int VEC, bool HALF, bool WIDE>
+int launch_rotary_t(RotParams &p, bool copy_rest, cudaStream_t stream) {
+  const int pairs = p.rot / 2;
+  p.rot_units = HALF ? pairs / VEC : p.rot / VEC;
+  p.units = p.rot_units + (copy_rest ? (p.dim - p.rot) / VEC : 0);
+  p.bx = p.units < kRotThreads ? p.units : kRotThreads;
+  p.by = kRotThreads / p.bx;
+  // enough tokens that every thread has a few units, fewer while the blocks
+  // would not fill the SMs
+  const int64_t total = static_cast<int64_t>(p.batch) * p.tokens;
+  int64_t nt = cdiv(int64_t{kRotThreads} * kRotUnroll, static_cast<int64_t>(p.units) * p.total_heads);
+  if (nt > kRotMaxTokens) nt = kRotMaxTokens;
+  while (nt > 1 && cdiv(total, nt) < 4 * 148) nt /= 2;
+  p.block_tokens = static_cast<int32_t>(nt);
+  const size_t smem = static_cast<size_t>(nt) * pairs * sizeof(float2);
+  return launch(rotary_kernel<T, VEC, HALF, WIDE>, dim3(static_cast<unsigned>(cdiv(total, nt))),
+                dim3(kRotThreads), smem, stream, p);
+}
+
+template <typename T>
+int launch_rotary(RotParams &p, int layout, bool copy_rest, bool wide, cudaStream_t stream) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T));
+  if (layout == W8A8_ROTARY_HALF) {
+    if (wide && (p.rot / 2) % V == 0 && p.dim % V == 0)
+      return launch_rotary_t<T, V, true, true>(p, copy_rest, stream);
+    return launch_rotary_t<T, 1, true, false>(p, copy_rest, stream);
+  }
+  if (wide && p.rot % V == 0 && p.dim % V == 0)
+    return launch_rotary_t<T, V, false, true>(p, copy_rest, stream);
+  return launch_rotary_t<T, 2, false, false>(p, copy_rest, stream);
+}
+
+// ---------------------------------------------------------------- group norm
+
+// How [B, S, C] is cut: rows of tpr threads, rpi of them per block, and slabs
+// per sample.  About two blocks per SM of a B200, none with less than a
+// statistics batch of pixels per thread.
+struct NormCut {
+  int32_t tpr, rpi, threads;
+  int64_t slabs;
+};
+constexpr int64_t kNormBlocks = 2 * 148;
+
+NormCut norm_cut(int64_t B, int64_t S, int64_t C, int dtype) {
+  NormCut c;
+  c.tpr = static_cast<int32_t>(C / (16 / dtype_size(dtype)));
+  c.rpi = kNormThreads / c.tpr;
+  if (c.rpi > S) c.rpi = static_cast<int32_t>(S);
+  c.threads = static_cast<int32_t>(cdiv(static_cast<int64_t>(c.tpr) * c.rpi, 32) * 32);
+  c.slabs = cdiv(kNormBlocks, B);
+  const int64_t most = cdiv(S, static_cast<int64_t>(c.rpi) * kNormBatch);
+  if (c.slabs > most) c.slabs = most;
+  return c;
+}
+
+int check_norm(int64_t B, int64_t S, int64_t C, int64_t G, int dtype) {
+  if (B < 1 || S < 1 || C < 1 || G < 1 || C % G != 0) return W8A8_ERR_INVALID_ARG;
+  if (dtype < W8A8_DTYPE_BF16 || dtype > W8A8_DTYPE_FP32) return W8A8_ERR_INVALID_ARG;
+  if (C % 8 != 0 || C > (dtype == W8A8_DTYPE_FP32 ? 4 : 8) * kNormMaxVecs) return W8A8_ERR_UNSUPPORTED_SHAPE;
+  if (B > INT32_MAX / 2 || S > INT32_MAX / 2 || B * S > INT32_MAX / 2) return W8A8_ERR_UNSUPPORTED_SHAPE;
+  return W8A8_OK;
+}
+
+// Strides of a sample and a pixel: whole rows, 16-byte steps.
+int check_norm_strides(int64_t B, int64_t S, int64_t C, int64_t sb, int64_t ss) {
+  if ((S > 1 && ss < C) || (B > 1 && sb < C)) return W8A8_ERR_INVALID_ARG;
+  if (sb % 8 != 0 || ss % 8 != 0) return W8A8_ERR_UNSUPPORTED_SHAPE;
+  return W8A8_OK;
+}
+
+size_t norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, int dtype, bool backward) {
+  const NormCut c = norm_cut(B, S, C, dtype);
+  const size_t slots = static_cast<size_t>(B) * static_cast<size_t>(c.slabs);
+  return align256(slots * static_cast<size_t>(G) * sizeof(float2)) +
+         (backward ? align256(slots * static_cast<size_t>(C) * sizeof(float2)) : 0);
+}
+
+void norm_params(NormParams *p, const NormCut &c, int64_t B, int64_t S, int64_t C, int64_t G,
+                 const void *weight, const void *bias, int param_dtype, int silu, void *workspace) {
+  std::memset(p, 0, sizeof(*p));
+  p->B = static_cast<int32_t>(B);
+  p->S = static_cast<int32_t>(S);
+  p->C = static_cast<int32_t>(C);
+  p->G = static_cast<int32_t>(G);
+  p->slabs = static_cast<int32_t>(c.slabs);
+  p->tpr = c.tpr;
+  p->rpi = c.rpi;
+  p->weight = weight;
+  p->bias = bias;
+  p->param_f32 = param_dtype == W8A8_DTYPE_FP32 ? 1 : 0;
+  p->silu = silu;
+  p->part = static_cast<float2 *>(workspace);
+  p->chan = reinterpret_cast<float2 *>(
+      static_cast<uint8_t *>(workspace) +
+      align256(static_cast<size_t>(B) * static_cast<size_t>(c.slabs) * static_cast<size_t>(G) *
+               sizeof(float2)));
+}
+
+template <typename T, bool QUANT>
+int launch_norm(const NormParams &p, const NormCut &c, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.B * c.slabs));
+  const size_t stat_smem = static_cast<size_t>(p.rpi) * p.C * sizeof(float2);
+  int st = launch(norm_stats_kernel<T>, grid, dim3(c.threads), stat_smem, stream, p);
+  if (st != W8A8_OK) return st;
+  const size_t smem = static_cast<size_t>(p.G) * sizeof(float2) +
+                      (QUANT ? static_cast<size_t>(kNormRows) * p.rpi * sizeof(uint32_t) : 0);
+  return launch(norm_apply_kernel<T, QUANT>, grid, dim3(c.threads), smem, stream, p);
+}
+
+template <typename T>
+int launch_norm_grad(const NormParams &p, const NormCut &c, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.B * c.slabs));
+  const size_t sum_smem = static_cast<size_t>(p.rpi) * p.C * sizeof(float2);
+  int st = launch(norm_grad_sums_kernel<T>, grid, dim3(c.threads), sum_smem, stream, p);
+  if (st != W8A8_OK) return st;
+  if (p.dweight != nullptr || p.dbias != nullptr) {
+    st = launch(norm_grad_params_kernel, dim3(static_cast<unsigned>(cdiv(p.C, 8))), dim3(256), 0,
+                stream, p);
+    if (st != W8A8_OK) return st;
+  }
+  return launch(norm_grad_apply_kernel<T>, grid, dim3(c.threads),
+                static_cast<size_t>(p.G) * sizeof(float2), stream, p);
 }
 
 template <bool FUSED, bool RAW>
@@ -1487,6 +1802,290 @@ int w8a16_linear(const void *x, int64_t M, int64_t K, int64_t ldx, const int8_t 
   const int64_t grid = tiles < d->sms ? tiles : d->sms;
   return launch_ex(true, kernel, dim3(static_cast<unsigned>(grid)), dim3(kWtThreads),
                    L::kSmemBytes, reinterpret_cast<cudaStream_t>(stream), mx, mw, p);
+}
+
+// Shapes of the input gradient: the layer's own (K % 16, N % 8), with the
+// contraction along N bounded as the layer's is along K.
+static int check_input_grad(int64_t M, int64_t N, int64_t K, int64_t lddy, int64_t lddx) {
+  if (M < 1 || N < 1 || K < 1 || lddy < N || lddx < K) return W8A8_ERR_INVALID_ARG;
+  if (K % 16 != 0 || N % 8 != 0 || N > kMaxK || lddy % 8 != 0 || lddx % 8 != 0 ||
+      M > INT32_MAX / 2 || K > INT32_MAX / 2)
+    return W8A8_ERR_UNSUPPORTED_SHAPE;
+  return W8A8_OK;
+}
+
+int w8a8_input_grad_workspace_size(int64_t M, int64_t N, int64_t K, int variant, size_t *bytes) {
+  if (!bytes) return W8A8_ERR_INVALID_ARG;
+  int st = check_input_grad(M, N, K, N, K);
+  if (st != W8A8_OK) return st;
+  if (variant < W8A8_VARIANT_AUTO || variant > W8A8_VARIANT_GEMV_TC) return W8A8_ERR_INVALID_ARG;
+  w8a8_plan plan;
+  st = select_input_grad_plan(M, N, K, 148, variant, 232448, &plan);
+  if (st != W8A8_OK) return st;
+  *bytes = input_grad_head_bytes(M, N) + split_workspace_bytes(plan);
+  return W8A8_OK;
+}
+
+int w8a8_linear_input_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, const int8_t *Wq,
+                           const float *s_w, int64_t K, void *dx, int64_t lddx, int variant,
+                           void *workspace, size_t ws_bytes, w8a8_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (!dy || !Wq || !s_w || !dx) return W8A8_ERR_INVALID_ARG;
+  if (variant < W8A8_VARIANT_AUTO || variant > W8A8_VARIANT_GEMV_TC) return W8A8_ERR_INVALID_ARG;
+  int st = check_input_grad(M, N, K, lddy, lddx);
+  if (st != W8A8_OK) return st;
+  if (!aligned16(dy) || !aligned16(Wq) || !aligned16(s_w) || !aligned16(dx))
+    return W8A8_ERR_MISALIGNED;
+  const size_t head = input_grad_head_bytes(M, N);
+  if (!workspace || ws_bytes < head || !aligned16(workspace)) return W8A8_ERR_WORKSPACE;
+  const DeviceInfo *d = nullptr;
+  st = query_device(&d);
+  if (st != W8A8_OK) return st;
+  w8a8_plan plan;
+  st = select_input_grad_plan(M, N, K, d->sms, variant, d->max_smem_optin, &plan);
+  if (st != W8A8_OK) return st;
+  // workspace layout: [codes | s_g (M floats) | K-split region]
+  int8_t *codes = static_cast<int8_t *>(workspace);
+  float *s_g = reinterpret_cast<float *>(codes + (head - align256(static_cast<size_t>(M) * sizeof(float))));
+  const SplitRegion split = split_region(plan, codes + head, ws_bytes - head);
+  // cleared before the quantization kernel, so that the product stays its
+  // programmatic dependent
+  st = clear_counters(split.counters, split.counters ? split_counter_bytes(plan) : 0, stream);
+  if (st != W8A8_OK) return st;
+  st = launch_quant_grad(dy, M, N, lddy, s_w, codes, s_g, stream);
+  if (st != W8A8_OK) return st;
+  switch (plan.variant) {
+    case W8A8_VARIANT_GEMM_PAIR:
+      return launch_input_grad_pair(plan, codes, s_g, M, N, Wq, K, dx, lddx, split, stream);
+    case W8A8_VARIANT_GEMM_BN128:
+      return launch_input_grad_gemm<128, kGemmStages128>(plan, codes, s_g, M, N, Wq, K, dx, lddx, stream);
+    case W8A8_VARIANT_GEMM_BN256:
+      return launch_input_grad_gemm<256, kGemmStages256>(plan, codes, s_g, M, N, Wq, K, dx, lddx, stream);
+    default: break;
+  }
+  switch (plan.tile_n) {
+    case 16: return launch_input_grad_swap<16>(plan, codes, s_g, M, N, Wq, K, dx, lddx, stream);
+    case 32: return launch_input_grad_swap<32>(plan, codes, s_g, M, N, Wq, K, dx, lddx, stream);
+    case 64: return launch_input_grad_swap<64>(plan, codes, s_g, M, N, Wq, K, dx, lddx, stream);
+    default: return launch_input_grad_swap<128>(plan, codes, s_g, M, N, Wq, K, dx, lddx, stream);
+  }
+}
+
+int w8a8_rotary(const w8a8_rotary_heads *tensors, int num_tensors, int dtype, int64_t batch,
+                int64_t tokens, int64_t dim, int64_t rot, int layout, const void *positions,
+                int position_bits, int64_t pos_batch, int64_t pos_token, int64_t axes,
+                const double *inv_freq, const int32_t *axis, float scale, int backward,
+                w8a8_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (!tensors || num_tensors < 1 || num_tensors > 2 || !positions || !inv_freq)
+    return W8A8_ERR_INVALID_ARG;
+  if (dtype < W8A8_DTYPE_BF16 || dtype > W8A8_DTYPE_FP32) return W8A8_ERR_INVALID_ARG;
+  if (layout != W8A8_ROTARY_INTERLEAVED && layout != W8A8_ROTARY_HALF) return W8A8_ERR_INVALID_ARG;
+  if (position_bits != 32 && position_bits != 64) return W8A8_ERR_INVALID_ARG;
+  if (batch < 1 || tokens < 1 || dim < 1 || rot < 2 || rot > dim || axes < 1 || !(std::isfinite(scale)))
+    return W8A8_ERR_INVALID_ARG;
+  if (dim % 2 != 0 || rot % 2 != 0 || dim > kRotMaxDim || axes > kRotMaxAxes)
+    return W8A8_ERR_UNSUPPORTED_SHAPE;
+  if (batch > INT32_MAX / 2 || tokens > INT32_MAX / 2 || batch * tokens > INT32_MAX / 2)
+    return W8A8_ERR_UNSUPPORTED_SHAPE;
+  if (reinterpret_cast<uintptr_t>(positions) % (position_bits / 8) != 0) return W8A8_ERR_MISALIGNED;
+  RotParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int size = dtype_size(dtype), vec = 16 / size;
+  bool wide = true, in_place = true;
+  int64_t heads = 0;
+  for (int i = 0; i < num_tensors; ++i) {
+    const w8a8_rotary_heads &t = tensors[i];
+    if (!t.x || !t.y || t.heads < 1) return W8A8_ERR_INVALID_ARG;
+    if (t.heads > INT32_MAX / 4) return W8A8_ERR_UNSUPPORTED_SHAPE;
+    // every head of y is a place of its own
+    if ((batch > 1 && t.y_batch == 0) || (tokens > 1 && t.y_token == 0) || (t.heads > 1 && t.y_head == 0))
+      return W8A8_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(t.x) % size != 0 || reinterpret_cast<uintptr_t>(t.y) % size != 0)
+      return W8A8_ERR_MISALIGNED;
+    RotHeads &r = p.t[i];
+    r.x = t.x;
+    r.y = t.y;
+    r.heads = static_cast<int32_t>(t.heads);
+    r.xb = t.x_batch; r.xt = t.x_token; r.xh = t.x_head;
+    r.yb = t.y_batch; r.yt = t.y_token; r.yh = t.y_head;
+    heads += t.heads;
+    wide = wide && wide_rows(t.x, t.x_batch, t.x_token, t.x_head, vec) &&
+           wide_rows(t.y, t.y_batch, t.y_token, t.y_head, vec);
+    in_place = in_place && t.x == t.y && t.x_batch == t.y_batch && t.x_token == t.y_token &&
+               t.x_head == t.y_head;
+  }
+  p.total_heads = static_cast<int32_t>(heads);
+  p.batch = static_cast<int32_t>(batch);
+  p.tokens = static_cast<int32_t>(tokens);
+  p.dim = static_cast<int32_t>(dim);
+  p.rot = static_cast<int32_t>(rot);
+  p.pos = positions;
+  p.pos_is_64 = position_bits == 64 ? 1 : 0;
+  p.axes = static_cast<int32_t>(axes);
+  p.pos_b = pos_batch;
+  p.pos_t = pos_token;
+  p.scale = scale;
+  p.backward = backward ? 1 : 0;
+  for (int64_t i = 0; i < rot / 2; ++i) {
+    if (!std::isfinite(inv_freq[i]) || inv_freq[i] < 0.0) return W8A8_ERR_INVALID_ARG;
+    const int32_t a = axis ? axis[i] : 0;
+    if (a < 0 || a >= axes) return W8A8_ERR_INVALID_ARG;
+    p.freq[i] = turns_q64(inv_freq[i]);
+    p.axis[i] = static_cast<uint8_t>(a);
+  }
+  const DeviceInfo *d = nullptr;
+  int st = query_device(&d);
+  if (st != W8A8_OK) return st;
+  switch (dtype) {
+    case W8A8_DTYPE_BF16: return launch_rotary<__nv_bfloat16>(p, layout, !in_place, wide, stream);
+    case W8A8_DTYPE_FP16: return launch_rotary<__half>(p, layout, !in_place, wide, stream);
+    default: return launch_rotary<float>(p, layout, !in_place, wide, stream);
+  }
+}
+
+int w8a8_group_norm_workspace_size(int64_t B, int64_t S, int64_t C, int64_t G, int dtype,
+                                   int backward, size_t *bytes) {
+  if (!bytes) return W8A8_ERR_INVALID_ARG;
+  int st = check_norm(B, S, C, G, dtype);
+  if (st != W8A8_OK) return st;
+  *bytes = norm_workspace_bytes(B, S, C, G, dtype, backward != 0);
+  return W8A8_OK;
+}
+
+// Checks that the forward forms and the gradient share.
+static int check_norm_call(int64_t B, int64_t S, int64_t C, int64_t G, int dtype, const void *weight,
+                           const void *bias, int param_dtype, int activation, const void *workspace,
+                           size_t ws_bytes, bool backward) {
+  int st = check_norm(B, S, C, G, dtype);
+  if (st != W8A8_OK) return st;
+  if (param_dtype != dtype && param_dtype != W8A8_DTYPE_FP32) return W8A8_ERR_INVALID_ARG;
+  if (activation != W8A8_ACT_NONE && activation != W8A8_ACT_SILU) return W8A8_ERR_INVALID_ARG;
+  const uintptr_t psize = static_cast<uintptr_t>(dtype_size(param_dtype));
+  if (reinterpret_cast<uintptr_t>(weight) % psize != 0 || reinterpret_cast<uintptr_t>(bias) % psize != 0)
+    return W8A8_ERR_MISALIGNED;
+  if (!workspace || !aligned16(workspace) ||
+      ws_bytes < norm_workspace_bytes(B, S, C, G, dtype, backward))
+    return W8A8_ERR_WORKSPACE;
+  return W8A8_OK;
+}
+
+int w8a8_group_norm(const void *x, int64_t x_batch, int64_t x_pixel, int dtype, int64_t B, int64_t S,
+                    int64_t C, int64_t G, const void *weight, const void *bias, int param_dtype,
+                    float eps, int activation, void *y, int64_t y_batch, int64_t y_pixel,
+                    float *mean_out, float *rstd_out, void *workspace, size_t ws_bytes,
+                    w8a8_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (!x || !y || !mean_out != !rstd_out || !(eps >= 0.0f)) return W8A8_ERR_INVALID_ARG;
+  int st = check_norm_call(B, S, C, G, dtype, weight, bias, param_dtype, activation, workspace,
+                           ws_bytes, false);
+  if (st != W8A8_OK) return st;
+  st = check_norm_strides(B, S, C, x_batch, x_pixel);
+  if (st != W8A8_OK) return st;
+  st = check_norm_strides(B, S, C, y_batch, y_pixel);
+  if (st != W8A8_OK) return st;
+  if (!aligned16(x) || !aligned16(y) || (reinterpret_cast<uintptr_t>(mean_out) & 3u) ||
+      (reinterpret_cast<uintptr_t>(rstd_out) & 3u))
+    return W8A8_ERR_MISALIGNED;
+  const DeviceInfo *d = nullptr;
+  st = query_device(&d);
+  if (st != W8A8_OK) return st;
+  const NormCut c = norm_cut(B, S, C, dtype);
+  NormParams p;
+  norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, activation == W8A8_ACT_SILU, workspace);
+  p.x = x;
+  p.xb = x_batch;
+  p.xs = x_pixel;
+  p.y = y;
+  p.yb = y_batch;
+  p.ys = y_pixel;
+  p.eps = eps;
+  p.mean_out = mean_out;
+  p.rstd_out = rstd_out;
+  switch (dtype) {
+    case W8A8_DTYPE_BF16: return launch_norm<__nv_bfloat16, false>(p, c, stream);
+    case W8A8_DTYPE_FP16: return launch_norm<__half, false>(p, c, stream);
+    default: return launch_norm<float, false>(p, c, stream);
+  }
+}
+
+int w8a8_group_norm_quant(const void *x_bf16, int64_t x_batch, int64_t x_pixel, int64_t B, int64_t S,
+                          int64_t C, int64_t G, const void *weight, const void *bias,
+                          int param_dtype, float eps, int activation, int8_t *q, float *s_a,
+                          float *mean_out, float *rstd_out, void *workspace, size_t ws_bytes,
+                          w8a8_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (!x_bf16 || !q || !s_a || !mean_out != !rstd_out || !(eps >= 0.0f)) return W8A8_ERR_INVALID_ARG;
+  int st = check_norm_call(B, S, C, G, W8A8_DTYPE_BF16, weight, bias, param_dtype, activation,
+                           workspace, ws_bytes, false);
+  if (st != W8A8_OK) return st;
+  if (C % 16 != 0) return W8A8_ERR_UNSUPPORTED_SHAPE;
+  st = check_norm_strides(B, S, C, x_batch, x_pixel);
+  if (st != W8A8_OK) return st;
+  if (!aligned16(x_bf16) || !aligned16(q) || (reinterpret_cast<uintptr_t>(s_a) & 3u) ||
+      (reinterpret_cast<uintptr_t>(mean_out) & 3u) || (reinterpret_cast<uintptr_t>(rstd_out) & 3u))
+    return W8A8_ERR_MISALIGNED;
+  const DeviceInfo *d = nullptr;
+  st = query_device(&d);
+  if (st != W8A8_OK) return st;
+  const NormCut c = norm_cut(B, S, C, W8A8_DTYPE_BF16);
+  NormParams p;
+  norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, activation == W8A8_ACT_SILU, workspace);
+  p.x = x_bf16;
+  p.xb = x_batch;
+  p.xs = x_pixel;
+  p.eps = eps;
+  p.q = q;
+  p.s_q = s_a;
+  p.mean_out = mean_out;
+  p.rstd_out = rstd_out;
+  return launch_norm<__nv_bfloat16, true>(p, c, stream);
+}
+
+int w8a8_group_norm_backward(const void *dy, int64_t dy_batch, int64_t dy_pixel, const void *x,
+                             int64_t x_batch, int64_t x_pixel, int dtype, int64_t B, int64_t S,
+                             int64_t C, int64_t G, const float *mean, const float *rstd,
+                             const void *weight, const void *bias, int param_dtype, int activation,
+                             void *dx, int64_t dx_batch, int64_t dx_pixel, float *dweight,
+                             float *dbias, void *workspace, size_t ws_bytes, w8a8_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (!dy || !x || !mean || !rstd || !dx) return W8A8_ERR_INVALID_ARG;
+  int st = check_norm_call(B, S, C, G, dtype, weight, bias, param_dtype, activation, workspace,
+                           ws_bytes, true);
+  if (st != W8A8_OK) return st;
+  const int64_t strides[3][2] = {{dy_batch, dy_pixel}, {x_batch, x_pixel}, {dx_batch, dx_pixel}};
+  for (const auto &v : strides) {
+    st = check_norm_strides(B, S, C, v[0], v[1]);
+    if (st != W8A8_OK) return st;
+  }
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(dx) ||
+      ((reinterpret_cast<uintptr_t>(mean) | reinterpret_cast<uintptr_t>(rstd) |
+        reinterpret_cast<uintptr_t>(dweight) | reinterpret_cast<uintptr_t>(dbias)) & 3u))
+    return W8A8_ERR_MISALIGNED;
+  const DeviceInfo *d = nullptr;
+  st = query_device(&d);
+  if (st != W8A8_OK) return st;
+  const NormCut c = norm_cut(B, S, C, dtype);
+  NormParams p;
+  norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, activation == W8A8_ACT_SILU, workspace);
+  p.dy = dy;
+  p.dyb = dy_batch;
+  p.dys = dy_pixel;
+  p.x = x;
+  p.xb = x_batch;
+  p.xs = x_pixel;
+  p.y = dx;
+  p.yb = dx_batch;
+  p.ys = dx_pixel;
+  p.mean_in = mean;
+  p.rstd_in = rstd;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  switch (dtype) {
+    case W8A8_DTYPE_BF16: return launch_norm_grad<__nv_bfloat16>(p, c, stream);
+    case W8A8_DTYPE_FP16: return launch_norm_grad<__half>(p, c, stream);
+    default: return launch_norm_grad<float>(p, c, stream);
+  }
 }
 
 int w8a8_last_device_error(w8a8_stream_t stream) {

@@ -269,7 +269,7 @@ __device__ __forceinline__ bool mbar_wait_drain(uint64_t *bar, uint32_t parity) 
 // proper.
 constexpr int kEpiNormal = 0, kEpiWritePartial = 1, kEpiAddPartials = 2;
 
-template <int COLS, bool RAW_OUT>
+template <int COLS, bool RAW_OUT, bool COL_SCALE = true>
 __device__ __forceinline__ void epilogue_warp_slice(const GemmParams &p, const CUtensorMap *tmap_y,
                                                     uint32_t t_row, int row0, int col_base,
                                                     uint8_t *stage_buf, uint32_t &chunk_count,
@@ -332,7 +332,7 @@ __device__ __forceinline__ void epilogue_warp_slice(const GemmParams &p, const C
       float sw[32];
       uint32_t bw[16];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < (COL_SCALE ? 4 : 0); ++g) {
         const int cg = col0 + 8 * g;
         if (cg < p.N) {
           const float4 w0 = __ldg(reinterpret_cast<const float4 *>(p.s_w + cg));
@@ -376,8 +376,8 @@ __device__ __forceinline__ void epilogue_warp_slice(const GemmParams &p, const C
         float2 v = make_float2(__int2float_rn(static_cast<int32_t>(r[2 * i])),
                                __int2float_rn(static_cast<int32_t>(r[2 * i + 1])));
         v = mul2_rn(v, sa2);
-        v = mul2_rn(v, make_float2(sw[2 * i], sw[2 * i + 1]));
-        if (p.bias != nullptr)
+        if constexpr (COL_SCALE) v = mul2_rn(v, make_float2(sw[2 * i], sw[2 * i + 1]));
+        if (COL_SCALE && p.bias != nullptr)
           v = add2_rn(v, make_float2(__uint_as_float(bw[i] << 16),
                                      __uint_as_float(bw[i] & 0xFFFF0000u)));
         const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
@@ -407,7 +407,12 @@ __device__ __forceinline__ void epilogue_warp_slice(const GemmParams &p, const C
   }
 }
 
-template <int BN, int STAGES, bool RAW_OUT>
+// B_MN: the input-gradient form.  The contraction runs over the rows of Wq as
+// it is stored ([contraction, columns of y], columns contiguous), so its tiles
+// are MN-major MMA operands, loaded as boxes of 128 columns x kBK contraction
+// rows; p.N counts the columns of Wq, p.K its rows, and the epilogue has
+// neither column scales nor a bias.
+template <int BN, int STAGES, bool RAW_OUT, bool B_MN = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_i8_tcgen05_kernel(const __grid_constant__ CUtensorMap tmap_a,
                            const __grid_constant__ CUtensorMap tmap_b,
@@ -426,6 +431,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  static_assert(!B_MN || BN % 128 == 0, "MN-major boxes are 128 columns wide");
+  // k-block kb of column block nb of the weights into a stage
+  auto load_b = [&](uint64_t *bar, uint8_t *sb, int kb, int nb) {
+    if constexpr (B_MN) {
+#pragma unroll
+      for (int h = 0; h < BN / 128; ++h)
+        tma_load_2d(&tmap_b, bar, sb + h * 128 * kBK, nb * BN + h * 128, kb * kBK);
+    } else {
+      tma_load_2d(&tmap_b, bar, sb, kb * kBK, nb * BN);
+    }
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -470,7 +486,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int kb = 0; kb < prefetched; ++kb) {
           uint8_t *sb = smem + kb * L::kStageBytes + L::kABytes;
           mbar_arrive_expect_tx(&full[kb], L::kStageBytes);
-          tma_load_2d(&tmap_b, &full[kb], sb, kb * kBK, nb0 * BN);
+          load_b(&full[kb], sb, kb, nb0);
         }
       }
       grid_dependency_wait();
@@ -488,7 +504,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             --prefetched;  // this stage's barrier is armed and its Wq tile is in flight
           } else {
             mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
-            tma_load_2d(&tmap_b, &full[stage], sb, kb * kBK, nb * BN);
+            load_b(&full[stage], sb, kb, nb);
           }
           tma_load_2d(&tmap_a, &full[stage], sa, kb * kBK, mb * kBM);
           ++issued;
@@ -509,7 +525,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_i8(kBM, BN);
+      constexpr uint32_t idesc = idesc_i8(kBM, BN) | (B_MN ? kIdescBMajorMN : 0u);
+      constexpr uint32_t kBStep = B_MN ? (kMmaK * 128) >> 4 : kMmaK >> 4;  // one MMA along K
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -531,11 +548,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           tc_fence_after();
           const uint32_t sa = smem_addr(smem + stage * L::kStageBytes);
           const uint64_t adesc = smem_desc_k_sw128(sa);
-          const uint64_t bdesc = smem_desc_k_sw128(sa + L::kABytes);
+          const uint64_t bdesc = B_MN ? smem_desc_mn_sw128(sa + L::kABytes, 128 * kBK)
+                                      : smem_desc_k_sw128(sa + L::kABytes);
 #pragma unroll
           for (int k = 0; k < kBK / kMmaK; ++k) {
             // +32 bytes along K inside the swizzled row = +2 in the address field
-            mma_i8(d_tmem, adesc + 2u * k, bdesc + 2u * k, idesc, (kb | k) != 0 ? 1u : 0u);
+            mma_i8(d_tmem, adesc + 2u * k, bdesc + kBStep * k, idesc, (kb | k) != 0 ? 1u : 0u);
           }
           any_mma = true;
           mma_commit(&empty[stage]);
@@ -577,7 +595,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_fence_after();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(acc * BN + half * (BN / 2));
-      epilogue_warp_slice<BN / 2, RAW_OUT>(p, &tmap_y, t_row, mb * kBM + quarter * 32,
+      epilogue_warp_slice<BN / 2, RAW_OUT, !B_MN>(p, &tmap_y, t_row, mb * kBM + quarter * 32,
                                            nb * BN + half * (BN / 2), stage_buf, chunk_count,
                                            lane);
       tc_fence_before();
@@ -641,7 +659,9 @@ __device__ __forceinline__ void pair_tile_coords(int t, const GemmParams &p, int
   gemm_tile_coords(t, p, mb, nb);  // p.num_m_blk counts 256-row blocks here
 }
 
-template <int STAGES, bool RAW_OUT, bool FUSE_QUANT>
+// B_MN: as in gemm_i8_tcgen05_kernel; a CTA's B half is one box of 128 columns.
+// A narrow tail tile loads a whole box too and uses its first 64 columns.
+template <int STAGES, bool RAW_OUT, bool FUSE_QUANT, bool B_MN = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm_i8_tcgen05_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                                 const __grid_constant__ CUtensorMap tmap_b,
@@ -717,7 +737,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         return nb * kPairBN + it.n_off + static_cast<int>(rank) * (it.ncols / 2);
       };
       auto stage_tx = [&](const WorkItem &it) {
+        if constexpr (B_MN) return 2u * static_cast<uint32_t>(L::kStageBytes);
         return 2u * static_cast<uint32_t>(L::kABytes + (it.ncols / 2) * kBK);
+      };
+      auto load_b = [&](const WorkItem &it, uint32_t bar, uint8_t *sb, int kb, int nb) {
+        if constexpr (B_MN)
+          tma_load_2d_pair(&tmap_b, bar, sb, b_row(it, nb), kb * kBK);
+        else
+          tma_load_2d_pair(b_map(it), bar, sb, kb * kBK, b_row(it, nb));
       };
       // fused quantization: the epilogue warps use the ring for their first
       // rows; nothing is loaded into it before they are all done with it
@@ -730,8 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         for (int i = 0; i < prefetched; ++i) {
           uint8_t *sb = smem + i * L::kStageBytes + L::kABytes;
           if (rank == 0) mbar_arrive_expect_tx(&full[i], stage_tx(w));
-          tma_load_2d_pair(b_map(w), map_to_cta(smem_addr(&full[i]), 0), sb,
-                           (w.kb_begin + i) * kBK, b_row(w, nb0));
+          load_b(w, map_to_cta(smem_addr(&full[i]), 0), sb, w.kb_begin + i, nb0);
         }
       }
       grid_dependency_wait();
@@ -761,7 +787,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             --prefetched;  // armed and Wq in flight already
           } else {
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], stage_tx(w));
-            tma_load_2d_pair(b_map(w), leader_full, sb, kb * kBK, b_row(w, nb));
+            load_b(w, leader_full, sb, kb, nb);
           }
           tma_load_2d_pair(&tmap_a, leader_full, sa, kb * kBK, mb * 256 + static_cast<int>(rank) * 128);
           ++issued;
@@ -795,7 +821,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kPairBN);
-        const uint32_t idesc = idesc_i8(2 * kBM, w.ncols);
+        const uint32_t idesc = idesc_i8(2 * kBM, w.ncols) | (B_MN ? kIdescBMajorMN : 0u);
+        constexpr uint32_t kBStep = B_MN ? (kMmaK * 128) >> 4 : kMmaK >> 4;
         for (int kb = w.kb_begin; kb < w.kb_end; ++kb) {
           if (!mbar_wait(&full[stage], phase, abort_flag)) {
             ok = false;
@@ -804,10 +831,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           tc_fence_after();
           const uint32_t sa = smem_addr(smem + stage * L::kStageBytes);
           const uint64_t adesc = smem_desc_k_sw128(sa);
-          const uint64_t bdesc = smem_desc_k_sw128(sa + L::kABytes);
+          const uint64_t bdesc = B_MN ? smem_desc_mn_sw128(sa + L::kABytes, 128 * kBK)
+                                      : smem_desc_k_sw128(sa + L::kABytes);
 #pragma unroll
           for (int k = 0; k < kBK / kMmaK; ++k)
-            mma_i8_pair(d_tmem, adesc + 2u * k, bdesc + 2u * k, idesc,
+            mma_i8_pair(d_tmem, adesc + 2u * k, bdesc + kBStep * k, idesc,
                         (kb != w.kb_begin || k != 0) ? 1u : 0u);
           any_mma = true;
           mma_commit_pair(&empty[stage], 0x3);
@@ -865,7 +893,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const int row0 = mb * 256 + static_cast<int>(rank) * 128 + quarter * 32;
       const int col_base = nb * kPairBN + w.n_off + half * wcols;
       if (w.nparts == 1) {
-        epilogue_warp_slice<kPairBN / 2, RAW_OUT>(p, &tmap_y, t_row, row0, col_base, stage_buf,
+        epilogue_warp_slice<kPairBN / 2, RAW_OUT, !B_MN>(p, &tmap_y, t_row, row0, col_base, stage_buf,
                                                   chunk_count, lane, kEpiNormal, nullptr, 0, 0, 0,
                                                   wcols);
       } else {
@@ -882,7 +910,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         __syncwarp();  // orders the lanes' partial-sum reads after lane 0's acquire
         last = __shfl_sync(0xFFFFFFFFu, last, 0);
         if (!last) {
-          epilogue_warp_slice<kPairBN / 2, RAW_OUT>(
+          epilogue_warp_slice<kPairBN / 2, RAW_OUT, !B_MN>(
               p, &tmap_y, t_row, row0, col_base, stage_buf, chunk_count, lane, kEpiWritePartial,
               first_slice + static_cast<int64_t>(w.part) * kSlicesPerTile * kSlotInts);
           __threadfence();
@@ -894,7 +922,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (last) {
           __threadfence();
           if (lane == 0) *reinterpret_cast<volatile unsigned long long *>(counter) = 0ull;
-          epilogue_warp_slice<kPairBN / 2, RAW_OUT>(
+          epilogue_warp_slice<kPairBN / 2, RAW_OUT, !B_MN>(
               p, &tmap_y, t_row, row0, col_base, stage_buf, chunk_count, lane, kEpiAddPartials,
               first_slice, w.nparts, w.part, static_cast<int64_t>(kSlicesPerTile) * kSlotInts);
         }

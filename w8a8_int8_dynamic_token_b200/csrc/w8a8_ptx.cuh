@@ -356,6 +356,24 @@ __device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t saddr) {
          (static_cast<uint64_t>(2u) << 61);
 }
 
+// Shared-memory matrix descriptor for an operand whose rows (M or N) run
+// along the contiguous dimension (MN-major), written by TMA with 128-byte
+// swizzling as boxes of 128 int8 (rows) x kBK contraction steps: one 128-byte
+// line per contraction step, groups of 8 steps 1024 bytes apart (the stride
+// byte offset), further blocks of 128 rows lead_bytes apart (the leading byte
+// offset; unused up to 128 rows).  The next 32 contraction steps start 4096
+// bytes on.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lead_bytes) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
+         (static_cast<uint64_t>((lead_bytes >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) |
+         (static_cast<uint64_t>(2u) << 61);
+}
+
+// Instruction-descriptor bits that mark A or B as MN-major (idesc_i8 | these).
+constexpr uint32_t kIdescAMajorMN = 1u << 15;
+constexpr uint32_t kIdescBMajorMN = 1u << 16;
+
 // Instruction descriptor, kind::i8: D s32 (bits 4-5 = 2), A and B signed int8
 // (bits 7-9 = 1, 10-12 = 1), both K-major (bits 15, 16 = 0), N >> 3 at bits
 // 17-22, M >> 4 at bits 24-28.

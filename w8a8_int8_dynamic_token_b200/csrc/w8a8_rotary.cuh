@@ -1,0 +1,196 @@
+// w8a8_rotary.cuh -- rotary positions on the heads a projection wrote.
+//
+// A head's first `rot` values are pairs (a, b): values i and i + rot / 2 in
+// the half layout, 2i and 2i + 1 in the interleaved one.  Pair i of the token
+// at position pos (along the axis that pair follows) turns by t = pos * f_i:
+//   a' = scale * (a cos t - b sin t),   b' = scale * (a sin t + b cos t);
+// the values behind `rot` are copied.  The gradient is the transposed map
+// (t -> -t, the same scale).
+//
+// Angles.  A 32-bit product pos * f loses the angle of far positions, so the
+// frequencies are held as turns per position in 64-bit fixed point: pos * f
+// modulo one turn is then one wrapping 64-bit integer product, off by at most
+// |pos| * 2^-65 turns (1.5e-9 at 2^36), and its top 32 bits go to sincospif.
+//
+// Bound by memory: every value is read once and written once.  A block takes
+// a few tokens, computes their cosines and sines once into shared memory (one
+// sincospif per pair and token instead of one per pair, token and head), and
+// walks over the heads with each thread staying on its place within the head,
+// so the factors stay in registers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "w8a8_ptx.cuh"
+
+namespace w8a8 {
+
+constexpr int kRotMaxDim = 512;
+constexpr int kRotMaxPairs = kRotMaxDim / 2;
+constexpr int kRotMaxAxes = 8;
+constexpr int kRotThreads = 256;
+constexpr int kRotMaxTokens = 16;  // tokens a block takes at most
+constexpr int kRotUnroll = 4;      // heads in flight per thread
+
+// The heads of one tensor; strides in elements.
+struct RotHeads {
+  const void *x;
+  void *y;
+  int32_t heads;
+  int64_t xb, xt, xh, yb, yt, yh;
+};
+
+struct RotParams {
+  RotHeads t[2];
+  int32_t total_heads;    // of both tensors
+  int32_t batch, tokens;  // batch * tokens < 2^31
+  int32_t dim, rot;
+  int32_t block_tokens;   // tokens a block takes
+  int32_t units;          // a head's units of work: rotated ones, then copied ones
+  int32_t rot_units;
+  int32_t bx, by;         // threads along the units and along the heads
+  const void *pos;
+  int32_t pos_is_64, axes;
+  int64_t pos_b, pos_t;   // strides of pos in elements; its axes are adjacent
+  float scale;
+  int32_t backward;
+  unsigned long long freq[kRotMaxPairs];  // turns per position * 2^64
+  uint8_t axis[kRotMaxPairs];
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+
+// VEC values at p: one 16-byte access, or single values where WIDE is false.
+template <typename T, int VEC, bool WIDE>
+struct VecIO {
+  __device__ static __forceinline__ void load(const T *p, T (&v)[VEC]) {
+    if constexpr (WIDE) {
+      static_assert(sizeof(T) * VEC == 16, "one 16-byte access");
+      *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = p[i];
+    }
+  }
+  __device__ static __forceinline__ void store(T *p, const T (&v)[VEC]) {
+    if constexpr (WIDE) {
+      *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) p[i] = v[i];
+    }
+  }
+};
+
+// VEC: values of one access.  A unit is one access (interleaved, or copied
+// values) or the two accesses of the same pairs (half layout).
+template <typename T, int VEC, bool HALF, bool WIDE>
+__global__ void __launch_bounds__(kRotThreads)
+    rotary_kernel(const __grid_constant__ RotParams p) {
+  extern __shared__ float2 turn[];  // [block_tokens][rot / 2]: scale * (cos, sin)
+  using IO = VecIO<T, VEC, WIDE>;
+  constexpr int NP = HALF ? VEC : VEC / 2;  // pairs of a rotated unit
+  const int pairs = p.rot >> 1;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.block_tokens;
+  const int64_t left = static_cast<int64_t>(p.batch) * p.tokens - first;
+  const int nt = left < p.block_tokens ? static_cast<int>(left) : p.block_tokens;
+
+  for (int i = threadIdx.x; i < nt * pairs; i += kRotThreads) {
+    const int tt = i / pairs, pair = i - tt * pairs;
+    const int at = static_cast<int>(first) + tt;
+    const int b = at / p.tokens, tok = at - b * p.tokens;
+    const int64_t off = b * p.pos_b + tok * p.pos_t + p.axis[pair];
+    const long long pos = p.pos_is_64 ? static_cast<const long long *>(p.pos)[off]
+                                      : static_cast<const int *>(p.pos)[off];
+    const unsigned long long turns = static_cast<unsigned long long>(pos) * p.freq[pair];
+    // signed fraction of a turn in [-1/2, 1/2), twice it in half turns
+    const float half_turns = static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f;
+    float s, c;
+    sincospif(half_turns, &s, &c);
+    turn[i] = make_float2(c * p.scale, (p.backward ? -s : s) * p.scale);
+  }
+  __syncthreads();
+
+  const int tx = threadIdx.x % p.bx, ty = threadIdx.x / p.bx;
+  if (ty >= p.by) return;
+  for (int u = tx; u < p.units; u += p.bx) {
+    const bool rotated = u < p.rot_units;
+    // first value of the unit within the head
+    const int v0 = rotated ? u * VEC : p.rot + (u - p.rot_units) * VEC;
+    for (int tt = 0; tt < nt; ++tt) {
+      const int at = static_cast<int>(first) + tt;
+      const int b = at / p.tokens, tok = at - b * p.tokens;
+      float cs[NP], sn[NP];
+      if (rotated) {
+        const float2 *f = turn + tt * pairs + (HALF ? v0 : v0 >> 1);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const float2 v = f[i];
+          cs[i] = v.x;
+          sn[i] = v.y;
+        }
+      }
+      for (int h0 = ty; h0 < p.total_heads; h0 += kRotUnroll * p.by) {
+        T a[kRotUnroll][VEC], bb[HALF ? kRotUnroll : 1][VEC];
+        T *dst[kRotUnroll];
+#pragma unroll
+        for (int j = 0; j < kRotUnroll; ++j) {
+          const int h = h0 + j * p.by;
+          if (h >= p.total_heads) break;
+          const RotHeads &t = p.t[h >= p.t[0].heads ? 1 : 0];
+          const int hh = h >= p.t[0].heads ? h - p.t[0].heads : h;
+          const T *src = static_cast<const T *>(t.x) + b * t.xb + tok * t.xt + hh * t.xh + v0;
+          dst[j] = static_cast<T *>(t.y) + b * t.yb + tok * t.yt + hh * t.yh + v0;
+          IO::load(src, a[j]);
+          if constexpr (HALF) {
+            if (rotated) IO::load(src + pairs, bb[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kRotUnroll; ++j) {
+          const int h = h0 + j * p.by;
+          if (h >= p.total_heads) break;
+          if (rotated) {
+            if constexpr (HALF) {
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) {
+                const float x0 = to_f32<T>(a[j][i]), x1 = to_f32<T>(bb[j][i]);
+                a[j][i] = from_f32<T>(__fmaf_rn(x0, cs[i], -(x1 * sn[i])));
+                bb[j][i] = from_f32<T>(__fmaf_rn(x0, sn[i], x1 * cs[i]));
+              }
+              IO::store(dst[j] + pairs, bb[j]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < NP; ++i) {
+                const float x0 = to_f32<T>(a[j][2 * i]), x1 = to_f32<T>(a[j][2 * i + 1]);
+                a[j][2 * i] = from_f32<T>(__fmaf_rn(x0, cs[i], -(x1 * sn[i])));
+                a[j][2 * i + 1] = from_f32<T>(__fmaf_rn(x0, sn[i], x1 * cs[i]));
+              }
+            }
+          }
+          IO::store(dst[j], a[j]);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace w8a8

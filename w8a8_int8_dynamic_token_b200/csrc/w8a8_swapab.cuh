@@ -86,7 +86,7 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t local, uint32_t rank, uin
 // writes y[m, n] = bf16_rne(((float)acc * s_a[m]) * s_w[n] + (float)bias[n]).
 // s_a: the row scales, written by the preceding kernel.  All threads of the
 // CTA call it.
-template <int MPAD, bool RAW_OUT>
+template <int MPAD, bool RAW_OUT, bool COL_SCALE = true>
 __device__ __forceinline__ void swap_epilogue(const SwapParams &p, uint32_t tmem_base,
                                               uint64_t *tfull, volatile int *abort_flag,
                                               uint8_t *ring, int warp, int lane, int tile,
@@ -125,8 +125,8 @@ __device__ __forceinline__ void swap_epilogue(const SwapParams &p, uint32_t tmem
   if (epi && rank == 0 && ok) {
     grid_dependency_wait();  // s_a comes from the preceding kernel
     const bool n_ok = n < p.N;
-    const float sw = n_ok ? __ldg(p.s_w + n) : 0.0f;
-    const float bv = (n_ok && p.bias != nullptr)
+    const float sw = COL_SCALE && n_ok ? __ldg(p.s_w + n) : 0.0f;
+    const float bv = (COL_SCALE && n_ok && p.bias != nullptr)
                          ? __uint_as_float(static_cast<uint32_t>(__ldg(p.bias + n)) << 16)
                          : 0.0f;
 #pragma unroll 1
@@ -152,8 +152,11 @@ __device__ __forceinline__ void swap_epilogue(const SwapParams &p, uint32_t tmem
           p.acc_out[static_cast<int64_t>(m) * p.N + n] = static_cast<int32_t>(r[j]);
         } else {
           float v = __int2float_rn(static_cast<int32_t>(r[j]));
-          v = __fmul_rn(__fmul_rn(v, __ldcg(s_a + m)), sw);
-          if (p.bias != nullptr) v = __fadd_rn(v, bv);
+          v = __fmul_rn(v, __ldcg(s_a + m));
+          if constexpr (COL_SCALE) {
+            v = __fmul_rn(v, sw);
+            if (p.bias != nullptr) v = __fadd_rn(v, bv);
+          }
           const __nv_bfloat16 h = __float2bfloat16_rn(v);
           p.y[static_cast<int64_t>(m) * p.ldy + n] = *reinterpret_cast<const uint16_t *>(&h);
         }
@@ -162,7 +165,9 @@ __device__ __forceinline__ void swap_epilogue(const SwapParams &p, uint32_t tmem
   }
 }
 
-template <int MPAD, bool RAW_OUT>
+// A_MN: the input-gradient form (see gemm_i8_tcgen05_kernel): the tile's 128
+// rows are 128 columns of Wq, the contraction runs over its rows.
+template <int MPAD, bool RAW_OUT, bool A_MN = false>
 __global__ void __launch_bounds__(kSwThreads, 1)
     gemm_i8_swapab_kernel(const __grid_constant__ CUtensorMap tmap_w,
                           const __grid_constant__ CUtensorMap tmap_q, const SwapParams p) {
@@ -186,6 +191,14 @@ __global__ void __launch_bounds__(kSwThreads, 1)
   const int per = p.k_blocks / split, extra = p.k_blocks % split;
   const int kb0 = rank * per + (rank < extra ? rank : extra);
   const int kb1 = kb0 + per + (rank < extra ? 1 : 0);
+
+  // k-block kb of this tile's weights into a stage
+  auto load_w = [&](uint64_t *bar, uint8_t *dst, int kb) {
+    if constexpr (A_MN)
+      tma_load_2d(&tmap_w, bar, dst, tile * kBM, kb * kBK);
+    else
+      tma_load_2d(&tmap_w, bar, dst, kb * kBK, tile * kBM);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -220,7 +233,7 @@ __global__ void __launch_bounds__(kSwThreads, 1)
       const int pre = nkb < S ? nkb : S;
       for (int i = u; i < pre; i += 2) {
         mbar_arrive_expect_tx(&full[i], L::kStageBytes);
-        tma_load_2d(&tmap_w, &full[i], smem + i * L::kStageBytes, (kb0 + i) * kBK, tile * kBM);
+        load_w(&full[i], smem + i * L::kStageBytes, kb0 + i);
       }
       grid_dependency_wait();  // q is written by the preceding kernel
       int last = 0;            // one past the last k-block this thread issued
@@ -230,7 +243,7 @@ __global__ void __launch_bounds__(kSwThreads, 1)
         if (i >= S) {
           if (!mbar_wait(&empty[stage], static_cast<uint32_t>((i / S) & 1) ^ 1u, abort_flag)) break;
           mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
-          tma_load_2d(&tmap_w, &full[stage], sa, (kb0 + i) * kBK, tile * kBM);
+          load_w(&full[stage], sa, kb0 + i);
         }
         tma_load_2d(&tmap_q, &full[stage], sa + L::kABytes, (kb0 + i) * kBK, 0);
         last = i + 1;
@@ -247,7 +260,8 @@ __global__ void __launch_bounds__(kSwThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_i8(kBM, MPAD);
+      constexpr uint32_t idesc = idesc_i8(kBM, MPAD) | (A_MN ? kIdescAMajorMN : 0u);
+      constexpr uint32_t kAStep = A_MN ? (kMmaK * 128) >> 4 : kMmaK >> 4;  // one MMA along K
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true, any = false;
@@ -258,11 +272,12 @@ __global__ void __launch_bounds__(kSwThreads, 1)
         }
         tc_fence_after();
         const uint32_t sa = smem_addr(smem + stage * L::kStageBytes);
-        const uint64_t adesc = smem_desc_k_sw128(sa);
+        const uint64_t adesc =
+            A_MN ? smem_desc_mn_sw128(sa, L::kABytes) : smem_desc_k_sw128(sa);
         const uint64_t bdesc = smem_desc_k_sw128(sa + L::kABytes);
 #pragma unroll
         for (int k = 0; k < kBK / kMmaK; ++k)
-          mma_i8(tmem_base, adesc + 2u * k, bdesc + 2u * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+          mma_i8(tmem_base, adesc + kAStep * k, bdesc + 2u * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
         any = true;
         mma_commit(&empty[stage]);
         if (++stage == S) {
@@ -281,7 +296,7 @@ __global__ void __launch_bounds__(kSwThreads, 1)
   }
 
   // ---------------------------------------------------------------- epilogue
-  swap_epilogue<MPAD, RAW_OUT>(p, tmem_base, tfull, abort_flag, smem, warp, lane, tile, rank, split,
+  swap_epilogue<MPAD, RAW_OUT, !A_MN>(p, tmem_base, tfull, abort_flag, smem, warp, lane, tile, rank, split,
                                p.s_a);
   tc_fence_before();
   __syncthreads();
