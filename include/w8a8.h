@@ -393,7 +393,8 @@ typedef enum { W8A8_ACT_NONE = 0, W8A8_ACT_SILU = 1 } w8a8_activation;
  * be dy or x itself with the same strides.  Sums run in a fixed order: equal
  * inputs give equal bits.
  * C % 8 == 0, C <= 4096 (2048 in fp32), strides multiples of 8 and at least
- * C where their extent is above 1, B * S < 2^30, x, dy, y, q 16-byte aligned.
+ * C where their extent is above 1, B * S < 2^30, x, dy, y, q, weight, bias
+ * 16-byte aligned.
  * workspace: w8a8_group_norm_workspace_size bytes, 16-byte aligned, no
  * initialization needed.
  */

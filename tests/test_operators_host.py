@@ -170,7 +170,7 @@ def test_rotary_frequencies():
 
 # ----------------------------------------------------------------- group norm
 
-def norm(kind="norm", x=P, xb=640, xs=64, dtype=0, Bn=2, S=10, C=64, G=8, w=P, b=P, pdt=0, eps=1e-5, act=0, y=P, yb=640,
+def norm(kind="norm", x=P, xb=64000, xs=64, dtype=0, Bn=2, S=1000, C=64, G=8, w=P, b=P, pdt=0, eps=1e-5, act=0, y=P, yb=64000,
          ys=64, mean=None, rstd=None, ws=P, ws_bytes=BIG):
     if kind == "norm":
         return B.w8a8_group_norm(x, xb, xs, dtype, Bn, S, C, G, w, b, pdt, eps, act, y, yb, ys, mean, rstd, ws, ws_bytes, None)
@@ -184,7 +184,7 @@ def norm(kind="norm", x=P, xb=640, xs=64, dtype=0, Bn=2, S=10, C=64, G=8, w=P, b
 @pytest.mark.parametrize("change,expect", [
     ({"x": None}, INV), ({"y": None}, INV), ({"Bn": 0}, INV), ({"S": 0}, INV), ({"C": 0}, INV), ({"G": 0}, INV),
     ({"G": 7}, INV), ({"act": 2}, INV), ({"pdt": 1}, INV), ({"xs": 56}, INV), ({"xb": 56}, INV),
-    ({"C": 60, "G": 6}, SHAPE), ({"C": 4104, "xs": 4104, "xb": 41040}, SHAPE), ({"xs": 68}, SHAPE), ({"xb": 644}, SHAPE),
+    ({"C": 60, "G": 6}, SHAPE), ({"C": 4104, "xs": 4104, "xb": 4104000}, SHAPE), ({"xs": 68}, SHAPE), ({"xb": 64004}, SHAPE),
     ({"S": 1 << 30}, SHAPE), ({"Bn": 1 << 31}, SHAPE),
     ({"x": 264}, ALIGN), ({"y": 258}, ALIGN), ({"w": 257}, ALIGN), ({"b": 258, "w": None, "pdt": 2}, ALIGN),
     ({"ws": None}, WS), ({"ws_bytes": 8}, WS), ({"ws": 264}, WS),
@@ -196,14 +196,15 @@ def test_group_norm_refusals(kind, change, expect):
 def test_group_norm_more_refusals():
     assert norm(dtype=3) == INV and norm(eps=-1.0) == INV and norm(eps=math.nan) == INV
     assert norm(mean=P) == INV and norm(rstd=P) == INV and norm(mean=258, rstd=P) == ALIGN
-    assert norm(ys=56) == INV and norm(yb=56) == INV and norm(yb=644) == SHAPE
-    assert norm("quant", C=72, xs=72, xb=720) == SHAPE          # the int8 layer's K % 16
-    assert norm(dtype=2, pdt=2, C=2056, G=1, xs=2056, xb=20560, ys=2056, yb=20560) == SHAPE
+    assert norm(ys=56) == INV and norm(yb=56) == INV and norm(yb=64004) == SHAPE
+    assert norm("quant", C=72, xs=72, xb=72000) == SHAPE          # the int8 layer's K % 16
+    assert norm(dtype=2, pdt=2, C=2056, G=1, xs=2056, xb=2056000, ys=2056, yb=2056000) == SHAPE
 
 
 def test_group_norm_workspace():
-    one = w8a8.group_norm_workspace_size(1, 1, 64, 8)
-    assert one >= 8 * 8
+    assert w8a8.group_norm_workspace_size(1, 1, 64, 8) == 0        # one block: nothing to exchange
+    assert w8a8.group_norm_workspace_size(1, 1, 64, 8, torch.bfloat16, True) >= 64 * 8
+    assert w8a8.group_norm_workspace_size(2, 4096, 512, 32) >= 2 * 32 * 16
     assert w8a8.group_norm_workspace_size(2, 4096, 512, 32, torch.bfloat16, True) > \
         w8a8.group_norm_workspace_size(2, 4096, 512, 32)
     assert B.w8a8_group_norm_workspace_size(1, 1, 60, 1, 0, 0)[0] == SHAPE

@@ -1146,24 +1146,28 @@ int launch_rotary(RotParams &p, int layout, bool copy_rest, bool wide, cudaStrea
 
 // ---------------------------------------------------------------- group norm
 
-// How [B, S, C] is cut: rows of tpr threads, rpi of them per block, and slabs
-// per sample.  About two blocks per SM of a B200, none with less than a
-// statistics batch of pixels per thread.
+// How [B, S, C] is cut: rows of tpr threads, rpi of them at once, `rows` rows
+// per chunk, and slabs (blocks) per sample: the SMs over the samples, none
+// with less than a chunk.
 struct NormCut {
-  int32_t tpr, rpi, threads;
-  int64_t slabs;
+  int32_t tpr, rpi, run, rows;
+  int64_t slabs, teams;
 };
-constexpr int64_t kNormBlocks = 2 * 148;
+constexpr int64_t kNormBlocks = 148;  // the SMs of a B200
 
-NormCut norm_cut(int64_t B, int64_t S, int64_t C, int dtype) {
+NormCut norm_cut(int64_t B, int64_t S, int64_t C, int64_t G, int dtype, int mode, int64_t sms) {
   NormCut c;
-  c.tpr = static_cast<int32_t>(C / (16 / dtype_size(dtype)));
+  const int vec = 16 / dtype_size(dtype);
+  if (sms > kNormBlocks) sms = kNormBlocks;
+  c.tpr = static_cast<int32_t>(C / vec);
   c.rpi = kNormThreads / c.tpr;
   if (c.rpi > S) c.rpi = static_cast<int32_t>(S);
-  c.threads = static_cast<int32_t>(cdiv(static_cast<int64_t>(c.tpr) * c.rpi, 32) * 32);
-  c.slabs = cdiv(kNormBlocks, B);
-  const int64_t most = cdiv(S, static_cast<int64_t>(c.rpi) * kNormBatch);
-  if (c.slabs > most) c.slabs = most;
+  c.run = 1;
+  while (c.run < vec && (C / G) % (2 * c.run) == 0) c.run *= 2;
+  c.rows = c.rpi * (mode == kNormBackward ? kNormRows<kNormBackward> : kNormRows<kNormForward>);
+  c.slabs = B < sms ? sms / B : 1;
+  if (c.slabs > cdiv(S, c.rows)) c.slabs = cdiv(S, c.rows);
+  c.teams = sms / c.slabs < B ? sms / c.slabs : B;
   return c;
 }
 
@@ -1182,11 +1186,17 @@ int check_norm_strides(int64_t B, int64_t S, int64_t C, int64_t sb, int64_t ss) 
   return W8A8_OK;
 }
 
+// [entries | readers | channel sums]
+size_t norm_entry_bytes(const NormCut &c, int64_t B, int64_t G) {
+  return c.slabs > 1 ? align256(static_cast<size_t>(B) * G * c.slabs * sizeof(uint4)) : 0;
+}
+size_t norm_reader_bytes(const NormCut &c, int64_t B) {
+  return c.slabs > 1 ? align256(static_cast<size_t>(B) * c.slabs * sizeof(unsigned long long)) : 0;
+}
 size_t norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, int dtype, bool backward) {
-  const NormCut c = norm_cut(B, S, C, dtype);
-  const size_t slots = static_cast<size_t>(B) * static_cast<size_t>(c.slabs);
-  return align256(slots * static_cast<size_t>(G) * sizeof(float2)) +
-         (backward ? align256(slots * static_cast<size_t>(C) * sizeof(float2)) : 0);
+  const NormCut c = norm_cut(B, S, C, G, dtype, backward ? kNormBackward : kNormForward, kNormBlocks);
+  return norm_entry_bytes(c, B, G) + norm_reader_bytes(c, B) +
+         (backward ? align256(static_cast<size_t>(B) * c.slabs * C * sizeof(float2)) : 0);
 }
 
 void norm_params(NormParams *p, const NormCut &c, int64_t B, int64_t S, int64_t C, int64_t G,
@@ -1196,44 +1206,71 @@ void norm_params(NormParams *p, const NormCut &c, int64_t B, int64_t S, int64_t 
   p->S = static_cast<int32_t>(S);
   p->C = static_cast<int32_t>(C);
   p->G = static_cast<int32_t>(G);
-  p->slabs = static_cast<int32_t>(c.slabs);
   p->tpr = c.tpr;
   p->rpi = c.rpi;
+  p->run = c.run;
+  p->group_lanes = 32;
+  while (p->group_lanes > 1 && G * p->group_lanes > kNormThreads) p->group_lanes /= 2;
+  p->slabs = static_cast<int32_t>(c.slabs);
+  p->teams = static_cast<int32_t>(c.teams);
   p->weight = weight;
   p->bias = bias;
   p->param_f32 = param_dtype == W8A8_DTYPE_FP32 ? 1 : 0;
   p->silu = silu;
-  p->part = static_cast<float2 *>(workspace);
-  p->chan = reinterpret_cast<float2 *>(
-      static_cast<uint8_t *>(workspace) +
-      align256(static_cast<size_t>(B) * static_cast<size_t>(c.slabs) * static_cast<size_t>(G) *
-               sizeof(float2)));
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p->entries = reinterpret_cast<uint4 *>(ws);
+  p->readers = reinterpret_cast<unsigned long long *>(ws + norm_entry_bytes(c, B, G));
+  p->chan = reinterpret_cast<float2 *>(ws + norm_entry_bytes(c, B, G) + norm_reader_bytes(c, B));
+  p->tag = c.slabs > 1 ? next_tag(48) : 0;
+}
+
+// One launch.  Blocks that share a sample wait for one another, so the grid
+// (at most one block per SM) is launched cooperatively: all of it runs at once.
+template <typename T, int MODE>
+int launch_norm_mode(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaStream_t stream) {
+  const size_t region =
+      MODE == kNormBackward
+          ? static_cast<size_t>(p.C) * sizeof(float2) * (p.rpi > 2 ? p.rpi : 2)
+          : (static_cast<size_t>(p.rpi) * p.tpr * (kNormVec<T> / p.run) + p.G) * sizeof(float2) +
+                (MODE == kNormQuant ? 3 * static_cast<size_t>(c.rows) * sizeof(uint32_t) : 0);
+  p.chunk_bytes = c.rows * p.C * static_cast<int32_t>(sizeof(T));
+  const int64_t slot = static_cast<int64_t>(p.chunk_bytes) * (MODE == kNormBackward ? 2 : 1);
+  int64_t slots = (d.max_smem_optin - 1024 - static_cast<int64_t>(region)) / slot;
+  const int64_t chunks = cdiv(cdiv(p.S, c.slabs), c.rows);
+  if (slots > kNormMaxSlots) slots = kNormMaxSlots;
+  if (slots > chunks) slots = chunks;
+  p.slots = static_cast<int32_t>(slots);
+  constexpr auto kernel = norm_kernel<T, MODE>;
+  int st = ensure_smem_limit<kernel>(d.max_smem_optin - 1024);
+  if (st != W8A8_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(c.teams * c.slabs));
+  cfg.blockDim = dim3(kNormThreads + 32);
+  cfg.dynamicSmemBytes = static_cast<size_t>(slots * slot) + region;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = c.slabs > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return W8A8_ERR_CUDA;
+  }
+  return W8A8_OK;
 }
 
 template <typename T, bool QUANT>
-int launch_norm(const NormParams &p, const NormCut &c, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.B * c.slabs));
-  const size_t stat_smem = static_cast<size_t>(p.rpi) * p.C * sizeof(float2);
-  int st = launch(norm_stats_kernel<T>, grid, dim3(c.threads), stat_smem, stream, p);
-  if (st != W8A8_OK) return st;
-  const size_t smem = static_cast<size_t>(p.G) * sizeof(float2) +
-                      (QUANT ? static_cast<size_t>(kNormRows) * p.rpi * sizeof(uint32_t) : 0);
-  return launch(norm_apply_kernel<T, QUANT>, grid, dim3(c.threads), smem, stream, p);
+int launch_norm(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaStream_t stream) {
+  return launch_norm_mode<T, QUANT ? kNormQuant : kNormForward>(p, c, d, stream);
 }
 
 template <typename T>
-int launch_norm_grad(const NormParams &p, const NormCut &c, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.B * c.slabs));
-  const size_t sum_smem = static_cast<size_t>(p.rpi) * p.C * sizeof(float2);
-  int st = launch(norm_grad_sums_kernel<T>, grid, dim3(c.threads), sum_smem, stream, p);
-  if (st != W8A8_OK) return st;
-  if (p.dweight != nullptr || p.dbias != nullptr) {
-    st = launch(norm_grad_params_kernel, dim3(static_cast<unsigned>(cdiv(p.C, 8))), dim3(256), 0,
+int launch_norm_grad(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaStream_t stream) {
+  int st = launch_norm_mode<T, kNormBackward>(p, c, d, stream);
+  if (st != W8A8_OK || (p.dweight == nullptr && p.dbias == nullptr)) return st;
+  return launch(norm_grad_params_kernel, dim3(static_cast<unsigned>(cdiv(p.C, 8))), dim3(256), 0,
                 stream, p);
-    if (st != W8A8_OK) return st;
-  }
-  return launch(norm_grad_apply_kernel<T>, grid, dim3(c.threads),
-                static_cast<size_t>(p.G) * sizeof(float2), stream, p);
 }
 
 template <bool FUSED, bool RAW>
@@ -1961,12 +1998,9 @@ static int check_norm_call(int64_t B, int64_t S, int64_t C, int64_t G, int dtype
   if (st != W8A8_OK) return st;
   if (param_dtype != dtype && param_dtype != W8A8_DTYPE_FP32) return W8A8_ERR_INVALID_ARG;
   if (activation != W8A8_ACT_NONE && activation != W8A8_ACT_SILU) return W8A8_ERR_INVALID_ARG;
-  const uintptr_t psize = static_cast<uintptr_t>(dtype_size(param_dtype));
-  if (reinterpret_cast<uintptr_t>(weight) % psize != 0 || reinterpret_cast<uintptr_t>(bias) % psize != 0)
-    return W8A8_ERR_MISALIGNED;
-  if (!workspace || !aligned16(workspace) ||
-      ws_bytes < norm_workspace_bytes(B, S, C, G, dtype, backward))
-    return W8A8_ERR_WORKSPACE;
+  if ((weight && !aligned16(weight)) || (bias && !aligned16(bias))) return W8A8_ERR_MISALIGNED;
+  const size_t need = norm_workspace_bytes(B, S, C, G, dtype, backward);
+  if (need > 0 && (!workspace || !aligned16(workspace) || ws_bytes < need)) return W8A8_ERR_WORKSPACE;
   return W8A8_OK;
 }
 
@@ -1990,7 +2024,7 @@ int w8a8_group_norm(const void *x, int64_t x_batch, int64_t x_pixel, int dtype, 
   const DeviceInfo *d = nullptr;
   st = query_device(&d);
   if (st != W8A8_OK) return st;
-  const NormCut c = norm_cut(B, S, C, dtype);
+  const NormCut c = norm_cut(B, S, C, G, dtype, kNormForward, d->sms);
   NormParams p;
   norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, activation == W8A8_ACT_SILU, workspace);
   p.x = x;
@@ -2003,9 +2037,9 @@ int w8a8_group_norm(const void *x, int64_t x_batch, int64_t x_pixel, int dtype, 
   p.mean_out = mean_out;
   p.rstd_out = rstd_out;
   switch (dtype) {
-    case W8A8_DTYPE_BF16: return launch_norm<__nv_bfloat16, false>(p, c, stream);
-    case W8A8_DTYPE_FP16: return launch_norm<__half, false>(p, c, stream);
-    default: return launch_norm<float, false>(p, c, stream);
+    case W8A8_DTYPE_BF16: return launch_norm<__nv_bfloat16, false>(p, c, *d, stream);
+    case W8A8_DTYPE_FP16: return launch_norm<__half, false>(p, c, *d, stream);
+    default: return launch_norm<float, false>(p, c, *d, stream);
   }
 }
 
@@ -2028,7 +2062,7 @@ int w8a8_group_norm_quant(const void *x_bf16, int64_t x_batch, int64_t x_pixel, 
   const DeviceInfo *d = nullptr;
   st = query_device(&d);
   if (st != W8A8_OK) return st;
-  const NormCut c = norm_cut(B, S, C, W8A8_DTYPE_BF16);
+  const NormCut c = norm_cut(B, S, C, G, W8A8_DTYPE_BF16, kNormQuant, d->sms);
   NormParams p;
   norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, activation == W8A8_ACT_SILU, workspace);
   p.x = x_bf16;
@@ -2039,7 +2073,7 @@ int w8a8_group_norm_quant(const void *x_bf16, int64_t x_batch, int64_t x_pixel, 
   p.s_q = s_a;
   p.mean_out = mean_out;
   p.rstd_out = rstd_out;
-  return launch_norm<__nv_bfloat16, true>(p, c, stream);
+  return launch_norm<__nv_bfloat16, true>(p, c, *d, stream);
 }
 
 int w8a8_group_norm_backward(const void *dy, int64_t dy_batch, int64_t dy_pixel, const void *x,
@@ -2065,7 +2099,7 @@ int w8a8_group_norm_backward(const void *dy, int64_t dy_batch, int64_t dy_pixel,
   const DeviceInfo *d = nullptr;
   st = query_device(&d);
   if (st != W8A8_OK) return st;
-  const NormCut c = norm_cut(B, S, C, dtype);
+  const NormCut c = norm_cut(B, S, C, G, dtype, kNormBackward, d->sms);
   NormParams p;
   norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, activation == W8A8_ACT_SILU, workspace);
   p.dy = dy;
@@ -2082,9 +2116,9 @@ int w8a8_group_norm_backward(const void *dy, int64_t dy_batch, int64_t dy_pixel,
   p.dweight = dweight;
   p.dbias = dbias;
   switch (dtype) {
-    case W8A8_DTYPE_BF16: return launch_norm_grad<__nv_bfloat16>(p, c, stream);
-    case W8A8_DTYPE_FP16: return launch_norm_grad<__half>(p, c, stream);
-    default: return launch_norm_grad<float>(p, c, stream);
+    case W8A8_DTYPE_BF16: return launch_norm_grad<__nv_bfloat16>(p, c, *d, stream);
+    case W8A8_DTYPE_FP16: return launch_norm_grad<__half>(p, c, *d, stream);
+    default: return launch_norm_grad<float>(p, c, *d, stream);
   }
 }
 

@@ -10,48 +10,80 @@
 //   dw = sum dz * xh,  db = sum dz   (over samples and pixels)
 //   dx = rstd * (w dz - (1/n) sum w dz - xh * (1/n) sum w dz xh)
 //
-// Work is cut into (sample, run of pixels) slabs.  A thread keeps one 16-byte
-// vector of channels and walks over pixels, so a block reads whole rows.
-// Statistics: batches of 8 pixels per channel are reduced in two passes over
-// registers (mean, then squared deviations) and joined by the pairwise update
-// of Chan, Golub and LeVeque (1979); no difference of large squares appears,
-// so a mean far from zero costs no precision.  All joins run in a fixed order
-// (no atomics on sums): results do not depend on scheduling.
+// Every form needs a sum over a whole sample before it can write its first
+// value, and is bound by memory: one read of the inputs, one write.  One
+// launch does both passes.  A sample's pixels are cut into slabs, one per
+// block, one block per SM, all resident at once (a cooperative launch).  A
+// producer warp streams the slab through a ring of shared memory with bulk
+// copies; the 16 other warps reduce each chunk as it lands.  The last chunks
+// of the first pass stay in the ring, so a slab of up to 192 KB (28 MB over
+// the GPU) is read once; of longer ones the second pass, which runs backwards,
+// reads the rest again, the most recently read chunks first.
+//
+// Statistics: a thread keeps one 16-byte vector of channels; batches of rows
+// are reduced in two passes over registers (mean, then squared deviations)
+// and joined by the pairwise update of Chan, Golub and LeVeque (1979).  No
+// difference of large squares appears, so a mean far from zero costs no
+// precision.  All joins run in a fixed order (no atomics on sums): equal
+// inputs give equal bits.
+//
+// The blocks of a sample exchange (mean, squared deviations) or the gradient's
+// two sums per group through 16-byte entries that carry their launch's tag and
+// are read and written as one 128-bit access, so an entry is valid exactly
+// when its tag is: one round trip, no barrier and nothing to clear beforehand.
+// Each block marks (tagged too) that it has read them; the sample's first block
+// waits for the marks beside its second pass and takes all tags back, so a
+// replayed graph, whose launches carry the same tag, finds none of its own.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
+#include "w8a8_gemm.cuh"
 #include "w8a8_ptx.cuh"
 #include "w8a8_quant.cuh"
 #include "w8a8_rotary.cuh"
 
 namespace w8a8 {
 
-constexpr int kNormThreads = 512;  // at most; whole warps, rpi rows of tpr threads
+constexpr int kNormThreads = 512;  // consumers: rpi rows of tpr threads, the rest idle
+constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kNormMaxVecs = 512;  // 16-byte vectors of a pixel: 4096 channels, 2048 in fp32
-constexpr int kNormBatch = 8;  // pixels per statistics batch
-constexpr int kNormRows = 4;   // pixels in flight per thread elsewhere
+constexpr int kNormMaxSlots = 8;
+constexpr int kNormBar = 1;        // named barrier of the consumers
+
+// What a launch computes.
+constexpr int kNormForward = 0, kNormQuant = 1, kNormBackward = 2;
+// Rows of a chunk per thread.
+template <int MODE>
+constexpr int kNormRows = MODE == kNormBackward ? 2 : 4;
 
 struct NormParams {
   const void *x, *dy;
-  void *y;                       // y, or dx
+  void *y;                           // y, or dx
   int64_t xb, xs, dyb, dys, yb, ys;  // strides of a sample and a pixel, elements
   int32_t B, S, C, G;
-  int32_t slabs;                 // per sample
-  int32_t tpr, rpi;              // threads per row, rows per block iteration
-  const void *weight, *bias;     // [C] in x's type or fp32, or nullptr
+  int32_t tpr, rpi;                  // threads per row, rows per block iteration
+  int32_t run;                       // channels of a vector that surely share a group
+  int32_t group_lanes;               // threads joining a group: 32, fewer where groups are many
+  int32_t slabs;                     // blocks sharing a sample
+  int32_t teams;                     // samples in flight: gridDim.x / slabs
+  int32_t slots, chunk_bytes;        // of one tensor
+  const void *weight, *bias;         // [C] in x's type or fp32, 16-byte aligned, or nullptr
   int32_t param_f32;
   float eps;
   int32_t silu;
-  float2 *part;                  // [B][slabs][G]: (mean, M2), or the group sums
-  float2 *chan;                  // [B][slabs][C]: channel sums (backward)
-  float *mean_out, *rstd_out;    // [B, G] or nullptr
+  uint4 *entries;                    // [B][G][slabs] (slabs > 1)
+  unsigned long long *readers;       // [B][slabs] (slabs > 1)
+  unsigned long long tag;
+  float2 *chan;                      // [B][slabs][C]: channel sums (backward)
+  float *mean_out, *rstd_out;        // [B, G] or nullptr
   const float *mean_in, *rstd_in;
   int8_t *q;
   float *s_q;
-  float *dweight, *dbias;        // [C] or nullptr
+  float *dweight, *dbias;            // [C] or nullptr
 };
 
 // Pixels [lo, hi) of slab j: an even share, the first slabs one more.
@@ -61,24 +93,115 @@ __device__ __forceinline__ void slab_range(int S, int slabs, int j, int &lo, int
   hi = lo + per + (j < extra ? 1 : 0);
 }
 
-__device__ __forceinline__ float norm_param(const void *p, int f32, int c, float none,
-                                            const __nv_bfloat16 *) {
-  if (p == nullptr) return none;
-  return f32 ? static_cast<const float *>(p)[c] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[c]);
-}
-__device__ __forceinline__ float norm_param(const void *p, int f32, int c, float none,
-                                            const __half *) {
-  if (p == nullptr) return none;
-  return f32 ? static_cast<const float *>(p)[c] : __half2float(static_cast<const __half *>(p)[c]);
-}
-__device__ __forceinline__ float norm_param(const void *p, int, int c, float none, const float *) {
-  return p == nullptr ? none : static_cast<const float *>(p)[c];
-}
-
 template <typename T>
 constexpr int kNormVec = 16 / static_cast<int>(sizeof(T));
 
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+// A 16-byte vector as pairs of fp32 values, and back (rounded to nearest).
+template <typename T>
+struct Pairs;
+template <>
+struct Pairs<__nv_bfloat16> {
+  __device__ static __forceinline__ void get(uint4 v, float2 (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  __device__ static __forceinline__ uint4 put(const float2 (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[i].x, f[i].y);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Pairs<__half> {
+  __device__ static __forceinline__ void get(uint4 v, float2 (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+  }
+  __device__ static __forceinline__ uint4 put(const float2 (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(f[i].x, f[i].y);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Pairs<float> {
+  __device__ static __forceinline__ void get(uint4 v, float2 (&f)[2]) {
+    f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  __device__ static __forceinline__ uint4 put(const float2 (&f)[2]) {
+    return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                      __float_as_uint(f[1].y));
+  }
+};
+
+// The parameters of V adjacent channels from ch on (`none` where there are
+// none): one or two 16-byte loads, no load behind a branch on another's value.
+template <typename T>
+__device__ __forceinline__ void norm_param(const void *p, int f32, int ch, float none,
+                                           float2 (&out)[kNormVec<T> / 2]) {
+  constexpr int V = kNormVec<T>;
+  if (p == nullptr) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) out[i] = make_float2(none, none);
+  } else if (f32) {
+    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + ch);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const float4 v = __ldg(q + i);
+      out[2 * i] = make_float2(v.x, v.y);
+      out[2 * i + 1] = make_float2(v.z, v.w);
+    }
+  } else {
+    Pairs<T>::get(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + ch)), out);
+  }
+}
+
+// f(i, group of channel ch + i) for the V channels from ch on, c a group.
+template <int V, typename F>
+__device__ __forceinline__ void each_group(int ch, int c, F f) {
+  int g = ch / c, in = ch - g * c;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    f(i, g);
+    if (++in == c) {
+      in = 0;
+      ++g;
+    }
+  }
+}
+
+// Component i of an array of pairs.
+template <int H>
+__device__ __forceinline__ float &at(float2 (&v)[H], int i) {
+  return (i & 1) ? v[i >> 1].y : v[i >> 1].x;
+}
+
+// sigmoid of two values: 1 / (1 + 2^(-z log2 e)) with one reciprocal for
+// both, 1 / a = b / (a b), since the special-function unit (16 a clock and SM)
+// is what a second pass of exp and reciprocal per value would wait for.  The
+// exponent stops at 63 so that the product stays finite: the gate of a value
+// below -43.6 is 2^-63 instead of something smaller.
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+  const float2 t = mul2_rn(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  float e0, e1, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fminf(t.x, 63.0f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fminf(t.y, 63.0f)));
+  const float2 d = add2_rn(make_float2(e0, e1), make_float2(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
+  return mul2_rn(make_float2(r, r), make_float2(d.y, d.x));
+}
 
 // Sum over the warp in a fixed order.
 __device__ __forceinline__ float warp_sum(float v) {
@@ -87,311 +210,619 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Statistics of one slab: (mean, M2) of each group into part[b][slab][g].
-// Shared memory: float2 [rpi][C], then the row counts are arithmetic.
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads) norm_stats_kernel(const NormParams p) {
-  constexpr int V = kNormVec<T>;
-  extern __shared__ float2 chan_stat[];  // [rpi][C]
-  const int b = blockIdx.x / p.slabs, slab = blockIdx.x - b * p.slabs;
+__device__ __forceinline__ void entry_store(uint4 *p, float2 v, unsigned long long tag) {
+  const unsigned long long lo = (static_cast<unsigned long long>(__float_as_uint(v.y)) << 32) |
+                                __float_as_uint(v.x);
+  asm volatile("{\n\t.reg .b128 q;\n\tmov.b128 q, {%1, %2};\n\tst.relaxed.gpu.global.b128 [%0], q;\n\t}" ::"l"(p),
+               "l"(lo), "l"(tag)
+               : "memory");
+}
+
+__device__ __forceinline__ unsigned long long entry_load(const uint4 *p, float2 &v) {
+  unsigned long long lo, tag;
+  asm volatile("{\n\t.reg .b128 q;\n\tld.relaxed.gpu.global.b128 q, [%2];\n\tmov.b128 {%0, %1}, q;\n\t}"
+               : "=l"(lo), "=l"(tag)
+               : "l"(p)
+               : "memory");
+  v = make_float2(__uint_as_float(static_cast<uint32_t>(lo)), __uint_as_float(static_cast<uint32_t>(lo >> 32)));
+  return tag;
+}
+
+// The entry at p once it carries `tag` (bounded like every other wait).
+__device__ __forceinline__ bool entry_wait(const uint4 *p, unsigned long long tag, float2 &v,
+                                           volatile int *abort_flag) {
+  if (entry_load(p, v) == tag) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (entry_load(p, v) == tag) return true;
+    if ((i & 15u) == 0u) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(&g_device_error, W8A8_DEVERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ bool abort_seen(const int *flag) {
+  return *const_cast<const volatile int *>(flag) != 0;
+}
+
+// The producer warp's loads of one chunk: `rows` rows of `row_bytes` bytes,
+// `step` bytes apart, into dst (adjacent rows in one copy).
+__device__ __forceinline__ void norm_load_rows(uint8_t *dst, const uint8_t *src, int rows,
+                                               uint32_t row_bytes, int64_t step, uint64_t *bar,
+                                               int lane) {
+  if (step == static_cast<int64_t>(row_bytes)) {
+    if (lane == 0) bulk_load_g2s(dst, src, rows * row_bytes, bar);
+  } else {
+    for (int r = lane; r < rows; r += 32)
+      bulk_load_g2s(dst + r * row_bytes, src + r * step, row_bytes, bar);
+  }
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid_constant__ NormParams p) {
+  constexpr int V = kNormVec<T>, H = V / 2;  // values and pairs of a vector
+  constexpr int K = kNormRows<MODE>;
+  constexpr bool BWD = MODE == kNormBackward;
+  extern __shared__ __align__(128) uint8_t norm_smem[];
+  __shared__ uint64_t full[kNormMaxSlots], empty[kNormMaxSlots];
+  __shared__ int abort_flag;
+  const int NS = p.slots;
+  const int slot_bytes = p.chunk_bytes * (BWD ? 2 : 1);
+  // [slots][x rows, dy rows] | the statistics' region | row maxima (int8 form)
+  float2 *region = reinterpret_cast<float2 *>(norm_smem + NS * slot_bytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunk_rows = p.rpi * K;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.C) * sizeof(T);
+  const int team = blockIdx.x / p.slabs, slab = blockIdx.x - team * p.slabs;
   int lo, hi;
   slab_range(p.S, p.slabs, slab, lo, hi);
-  const int row = threadIdx.x / p.tpr, vec = threadIdx.x - row * p.tpr;
-  const T *x = static_cast<const T *>(p.x) + b * p.xb + vec * V;
-  float mean[V], m2[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) mean[i] = m2[i] = 0.0f;
-  int n = 0;
-  if (row < p.rpi) {
-    for (int s0 = lo + row; s0 < hi; s0 += kNormBatch * p.rpi) {
-      T v[kNormBatch][V];
-#pragma unroll
-      for (int j = 0; j < kNormBatch; ++j) {
-        const int s = s0 + j * p.rpi;
-        if (s < hi) VecIO<T, V, true>::load(x + s * p.xs, v[j]);
+  const int chunks = (hi - lo + chunk_rows - 1) / chunk_rows;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kNormWarps);
+    }
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+
+  if (warp == kNormWarps) {
+    // ------------------------------------------------------------ producer
+    uint32_t used = 0, empty_par = 0, full_par = 0;  // bit s: slot s
+    bool ok = true;
+    auto fill = [&](int b, int chunk) {
+      const int s = chunk % NS;
+      const uint32_t bit = 1u << s;
+      if (used & bit) {
+        ok = mbar_wait(&empty[s], (empty_par & bit) ? 1u : 0u, &abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return;
+        empty_par ^= bit;
+        full_par ^= bit;
       }
-      const int left = (hi - s0 + p.rpi - 1) / p.rpi;
-      const int nb = left < kNormBatch ? left : kNormBatch;
-      const float inv = 1.0f / nb;
-      const float share = static_cast<float>(nb) / static_cast<float>(n + nb);
-      const float cross = share * n;
+      used |= bit;
+      const int r0 = lo + chunk * chunk_rows;
+      const int rows = hi - r0 < chunk_rows ? hi - r0 : chunk_rows;
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], rows * row_bytes * (BWD ? 2u : 1u));
+      __syncwarp();
+      uint8_t *dst = norm_smem + s * slot_bytes;
+      norm_load_rows(dst, static_cast<const uint8_t *>(p.x) + (b * p.xb + r0 * p.xs) * static_cast<int64_t>(sizeof(T)),
+                     rows, row_bytes, p.xs * static_cast<int64_t>(sizeof(T)), &full[s], lane);
+      if constexpr (BWD)
+        norm_load_rows(dst + p.chunk_bytes,
+                       static_cast<const uint8_t *>(p.dy) + (b * p.dyb + r0 * p.dys) * static_cast<int64_t>(sizeof(T)),
+                       rows, row_bytes, p.dys * static_cast<int64_t>(sizeof(T)), &full[s], lane);
+    };
+    for (int b = team; ok && b < p.B; b += p.teams) {
+      for (int i = 0; ok && i < chunks; ++i) fill(b, i);
+      for (int i = chunks - NS - 1; ok && i >= 0; --i) fill(b, i);
+      if (p.slabs > 1 && slab == 0 && ok) {
+        // once every block has read the sample's entries: their tags go
+        for (int j = lane; j < p.slabs; j += 32) {
+          unsigned long long *r = p.readers + static_cast<int64_t>(b) * p.slabs + j;
+          const uint64_t t0 = global_timer_ns();
+          for (uint32_t i = 1; ok && ld_acquire_gpu_u64(r) != p.tag; ++i) {
+            if ((i & 15u) == 0u && (abort_seen(&abort_flag) || global_timer_ns() - t0 > kWaitLimitNs)) {
+              if (!abort_seen(&abort_flag)) atomicOr(&g_device_error, W8A8_DEVERR_TIMEOUT);
+              ok = false;
+            }
+          }
+          if (ok) *reinterpret_cast<volatile unsigned long long *>(r) = 0ull;
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        uint4 *e = p.entries + static_cast<int64_t>(b) * p.G * p.slabs;
+        for (int i = lane; ok && i < p.G * p.slabs; i += 32) entry_store(e + i, make_float2(0.0f, 0.0f), 0ull);
+      }
+    }
+    // copies still in flight (after an abort) land before the block leaves
+    for (int s = 0; s < NS; ++s) {
+      volatile int never = 0;
+      if (used & (1u << s)) mbar_wait(&full[s], (full_par >> s) & 1u, &never);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int tid = threadIdx.x;
+  const int row = tid / p.tpr, vec = tid - row * p.tpr;
+  const bool live = row < p.rpi;
+  const int c = p.C / p.G;
+  const uint32_t offset = static_cast<uint32_t>(row) * row_bytes + vec * 16u;
+  const uint32_t row_step = static_cast<uint32_t>(p.rpi) * row_bytes;
+  uint32_t full_par = 0;
+  bool ok = true;  // after a wait gave up the flow goes on, but stores nothing
+  auto arrive_full = [&](int s) {
+    if (ok) ok = mbar_wait(&full[s], (full_par >> s) & 1u, &abort_flag);
+    full_par ^= 1u << s;
+  };
+  auto release = [&](int s) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+  };
+
+  for (int b = team; b < p.B; b += p.teams) {
+    // gradient: per channel rstd, -mean, weight and bias
+    float2 rs[H], nm[H], wt[H], bs[H];
+    if constexpr (BWD) {
+      if (live) {
+        norm_param<T>(p.weight, p.param_f32, vec * V, 1.0f, wt);
+        norm_param<T>(p.bias, p.param_f32, vec * V, 0.0f, bs);
+        const int64_t at0 = static_cast<int64_t>(b) * p.G;
+        each_group<V>(vec * V, c, [&](int i, int g) {
+          at(nm, i) = -__ldg(p.mean_in + at0 + g);
+          at(rs, i) = __ldg(p.rstd_in + at0 + g);
+        });
+      }
+    }
+    // xh and dz of a vector (gradient)
+    auto grad_vec = [&](uint4 xv, uint4 gv, float2 (&xh)[H], float2 (&dz)[H]) {
+      Pairs<T>::get(xv, xh);
+      Pairs<T>::get(gv, dz);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float sum = 0.0f;
+      for (int i = 0; i < H; ++i) {
+        xh[i] = mul2_rn(add2_rn(xh[i], nm[i]), rs[i]);
+        if (p.silu) {  // y'(z) = s + z s (1 - s)
+          const float2 z = fma2_rn(xh[i], wt[i], bs[i]);
+          const float2 s = sigmoid2(z);
+          const float2 zs = mul2_rn(z, s);
+          const float2 d = add2_rn(s, fma2_rn(make_float2(-zs.x, -zs.y), s, zs));
+          dz[i] = mul2_rn(dz[i], d);
+        }
+      }
+    };
+
+    // ---- first pass: per channel (mean, squared deviations), or the two sums
+    float2 s1[H], s2[H];
 #pragma unroll
-        for (int j = 0; j < kNormBatch; ++j)
-          if (j < nb) sum += to_f32<T>(v[j][i]);
-        const float mb = sum * inv;
-        float sq = 0.0f;
+    for (int i = 0; i < H; ++i) s1[i] = s2[i] = make_float2(0.0f, 0.0f);
+    // One chunk's rows of this thread joined to the running values; `all`: K of
+    // them (every chunk but the last), else nb.
+    int n = 0;
+    auto reduce = [&](const uint8_t *src, int nb, auto all) {
+      constexpr bool ALL = decltype(all)::value;
+      if constexpr (BWD) {
+        float2 t1[H], t2[H];  // the chunk's sums join the running ones once
 #pragma unroll
-        for (int j = 0; j < kNormBatch; ++j) {
-          if (j < nb) {
-            const float d = to_f32<T>(v[j][i]) - mb;
-            sq += d * d;
+        for (int h = 0; h < H; ++h) t1[h] = t2[h] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (ALL || k < nb) {
+            float2 xh[H], dz[H];
+            grad_vec(*reinterpret_cast<const uint4 *>(src + k * row_step),
+                     *reinterpret_cast<const uint4 *>(src + p.chunk_bytes + k * row_step), xh, dz);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              t1[h] = add2_rn(t1[h], dz[h]);
+              t2[h] = fma2_rn(dz[h], xh[h], t2[h]);
+            }
           }
         }
-        const float delta = mb - mean[i];
-        mean[i] += delta * share;
-        m2[i] += sq + delta * delta * cross;
-      }
-      n += nb;
-    }
 #pragma unroll
-    for (int i = 0; i < V; ++i) chan_stat[row * p.C + vec * V + i] = make_float2(mean[i], m2[i]);
-  }
-  __syncthreads();
-  // a warp per group joins its rpi x c entries: entries of row r stand for
-  // n_r pixels
-  const int c = p.C / p.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int pixels = hi - lo;
-  const float inv_n = 1.0f / (static_cast<float>(pixels) * c);
-  for (int g = warp; g < p.G; g += warps) {
-    float sum = 0.0f;
-    for (int e = lane; e < p.rpi * c; e += 32) {
-      const int r = e / c, ch = g * c + (e - r * c);
-      const int nr = r < pixels ? (pixels - r + p.rpi - 1) / p.rpi : 0;
-      sum += nr * chan_stat[r * p.C + ch].x;
-    }
-    const float gm = warp_sum(sum) * inv_n;
-    float sq = 0.0f;
-    for (int e = lane; e < p.rpi * c; e += 32) {
-      const int r = e / c, ch = g * c + (e - r * c);
-      const int nr = r < pixels ? (pixels - r + p.rpi - 1) / p.rpi : 0;
-      const float2 st = chan_stat[r * p.C + ch];
-      const float d = st.x - gm;
-      sq += st.y + nr * d * d;
-    }
-    sq = warp_sum(sq);
-    if (lane == 0) p.part[(static_cast<int64_t>(b) * p.slabs + slab) * p.G + g] = make_float2(gm, sq);
-  }
-}
-
-// Joins a sample's slab statistics: (mean, rstd) of each group into out[G]
-// (shared memory).  All threads of the block call it; synchronizes at the end.
-__device__ __forceinline__ void norm_join(const NormParams &p, int b, float2 *out) {
-  const int c = p.C / p.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const float inv_s = 1.0f / p.S;
-  {
-    for (int g = warp; g < p.G; g += warps) {
-      const float2 *part = p.part + static_cast<int64_t>(b) * p.slabs * p.G + g;
-      float sum = 0.0f;
-      for (int j = lane; j < p.slabs; j += 32) {
-        int lo, hi;
-        slab_range(p.S, p.slabs, j, lo, hi);
-        sum += (hi - lo) * inv_s * part[static_cast<int64_t>(j) * p.G].x;
-      }
-      const float mean = warp_sum(sum);
-      float sq = 0.0f;
-      for (int j = lane; j < p.slabs; j += 32) {
-        int lo, hi;
-        slab_range(p.S, p.slabs, j, lo, hi);
-        const float2 st = part[static_cast<int64_t>(j) * p.G];
-        const float d = st.x - mean;
-        sq += st.y + static_cast<float>(hi - lo) * c * d * d;
-      }
-      const float var = warp_sum(sq) / (static_cast<float>(p.S) * c);
-      if (lane == 0) out[g] = make_float2(mean, 1.0f / sqrtf(var + p.eps));
-    }
-  }
-  __syncthreads();
-}
-
-// Normalizes one slab (see norm_stats_kernel for the mapping).  QUANT: int8
-// rows and their scales instead of y.
-template <typename T, bool QUANT>
-__global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const NormParams p) {
-  constexpr int V = kNormVec<T>;
-  constexpr int R = kNormRows;
-  extern __shared__ float2 group_stat[];  // [G]; QUANT: then uint [R * rpi] row maxima
-  const int b = blockIdx.x / p.slabs, slab = blockIdx.x - b * p.slabs;
-  int lo, hi;
-  slab_range(p.S, p.slabs, slab, lo, hi);
-  norm_join(p, b, group_stat);
-  const int c = p.C / p.G;
-  if (slab == 0 && p.mean_out != nullptr) {
-    for (int g = threadIdx.x; g < p.G; g += blockDim.x) {
-      p.mean_out[static_cast<int64_t>(b) * p.G + g] = group_stat[g].x;
-      p.rstd_out[static_cast<int64_t>(b) * p.G + g] = group_stat[g].y;
-    }
-  }
-  const int row = threadIdx.x / p.tpr, vec = threadIdx.x - row * p.tpr;
-  const bool live = row < p.rpi;
-  float scale[V], shift[V], mean[V];
-  if (live) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int ch = vec * V + i;
-      const float2 st = group_stat[ch / c];
-      mean[i] = st.x;
-      scale[i] = st.y * norm_param(p.weight, p.param_f32, ch, 1.0f, static_cast<const T *>(nullptr));
-      shift[i] = norm_param(p.bias, p.param_f32, ch, 0.0f, static_cast<const T *>(nullptr));
-    }
-  }
-  const T *x = static_cast<const T *>(p.x) + b * p.xb + vec * V;
-  if constexpr (!QUANT) {
-    if (!live) return;
-    T *y = static_cast<T *>(p.y) + b * p.yb + vec * V;
-    for (int s0 = lo + row; s0 < hi; s0 += R * p.rpi) {
-      T v[R][V];
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const int s = s0 + j * p.rpi;
-        if (s < hi) VecIO<T, V, true>::load(x + s * p.xs, v[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const int s = s0 + j * p.rpi;
-        if (s >= hi) break;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float z = __fmaf_rn(to_f32<T>(v[j][i]) - mean[i], scale[i], shift[i]);
-          v[j][i] = from_f32<T>(p.silu ? silu(z) : z);
+        for (int h = 0; h < H; ++h) {
+          s1[h] = add2_rn(s1[h], t1[h]);
+          s2[h] = add2_rn(s2[h], t2[h]);
         }
-        VecIO<T, V, true>::store(y + s * p.ys, v[j]);
-      }
-    }
-  } else {
-    uint32_t *row_max = reinterpret_cast<uint32_t *>(group_stat + p.G);  // [R * rpi]
-    for (int base = lo; base < hi; base += R * p.rpi) {  // block-uniform
-      for (int i = threadIdx.x; i < R * p.rpi; i += blockDim.x) row_max[i] = 0u;
-      __syncthreads();
-      float z[R][V];
+      } else {
+        float2 v[K][H];
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const int s = base + row + j * p.rpi;
-        if (!live || s >= hi) continue;
-        T v[V];
-        VecIO<T, V, true>::load(x + s * p.xs, v);
-        float m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float zz = __fmaf_rn(to_f32<T>(v[i]) - mean[i], scale[i], shift[i]);
-          z[j][i] = p.silu ? silu(zz) : zz;
-          m = fmaxf(m, fabsf(z[j][i]));
+        for (int k = 0; k < K; ++k) {
+          if (ALL || k < nb) Pairs<T>::get(*reinterpret_cast<const uint4 *>(src + k * row_step), v[k]);
         }
-        atomicMax(&row_max[row + j * p.rpi], __float_as_uint(m));  // order-independent
-      }
-      __syncthreads();
+        const float inv = ALL ? 1.0f / K : 1.0f / nb;
+        const float share = __fdividef(static_cast<float>(ALL ? K : nb), static_cast<float>(n + (ALL ? K : nb)));
+        const float cross = share * n;
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const int s = base + row + j * p.rpi;
-        if (!live || s >= hi) continue;
-        const float amax = __uint_as_float(row_max[row + j * p.rpi]);
-        const float sc = (amax == 0.0f) ? 0.0f : __fdiv_rn(amax, 127.0f);
-        const bool fast = quant_fast_ok(sc);
-        const float rc = fast ? __frcp_rn(sc) : 0.0f;
-        static_assert(V == 8, "int8 rows are made of bf16 activations");
-        uint32_t code[V];
+        for (int h = 0; h < H; ++h) {
+          float2 sum = v[0][h];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          code[i] = fast ? quant_fast(z[j][i], sc, rc) : quant_exact(z[j][i], sc);
-        const int64_t pix = static_cast<int64_t>(b) * p.S + s;
-        *reinterpret_cast<uint2 *>(p.q + pix * p.C + vec * V) =
-            sc == 0.0f ? make_uint2(0u, 0u) : pack_codes(code);
-        if (vec == 0) p.s_q[pix] = sc;
-      }
-      __syncthreads();
-    }
-  }
-}
-
-// y'(z) for SiLU: sigma + z sigma (1 - sigma).
-__device__ __forceinline__ float silu_grad(float z) {
-  const float sig = __fdividef(1.0f, 1.0f + __expf(-z));
-  return sig * (1.0f + z * (1.0f - sig));
-}
-
-// Backward sums of one slab: per channel (sum dz, sum dz xh) into chan, per
-// group (sum w dz, sum w dz xh) into part.
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_sums_kernel(const NormParams p) {
-  constexpr int V = kNormVec<T>;
-  constexpr int R = 4;
-  extern __shared__ float2 chan_sum[];  // [rpi][C]
-  const int b = blockIdx.x / p.slabs, slab = blockIdx.x - b * p.slabs;
-  int lo, hi;
-  slab_range(p.S, p.slabs, slab, lo, hi);
-  const int c = p.C / p.G;
-  const int row = threadIdx.x / p.tpr, vec = threadIdx.x - row * p.tpr;
-  if (row < p.rpi) {
-    float mean[V], rstd[V], w[V], bias[V];
+          for (int k = 1; k < K; ++k)
+            if (ALL || k < nb) sum = add2_rn(sum, v[k][h]);
+          const float2 mb = mul2_rn(sum, make_float2(inv, inv));
+          const float2 back = make_float2(-mb.x, -mb.y);
+          float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int ch = vec * V + i;
-      mean[i] = p.mean_in[static_cast<int64_t>(b) * p.G + ch / c];
-      rstd[i] = p.rstd_in[static_cast<int64_t>(b) * p.G + ch / c];
-      w[i] = norm_param(p.weight, p.param_f32, ch, 1.0f, static_cast<const T *>(nullptr));
-      bias[i] = norm_param(p.bias, p.param_f32, ch, 0.0f, static_cast<const T *>(nullptr));
-    }
-    const T *x = static_cast<const T *>(p.x) + b * p.xb + vec * V;
-    const T *dy = static_cast<const T *>(p.dy) + b * p.dyb + vec * V;
-    float s1[V], s2[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
-    for (int s0 = lo + row; s0 < hi; s0 += R * p.rpi) {
-      T xv[R][V], gv[R][V];
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const int s = s0 + j * p.rpi;
-        if (s < hi) {
-          VecIO<T, V, true>::load(x + s * p.xs, xv[j]);
-          VecIO<T, V, true>::load(dy + s * p.dys, gv[j]);
+          for (int k = 0; k < K; ++k) {
+            if (ALL || k < nb) {
+              const float2 d = add2_rn(v[k][h], back);
+              sq = fma2_rn(d, d, sq);
+            }
+          }
+          if (n == 0) {
+            s1[h] = mb;
+            s2[h] = sq;
+          } else {
+            const float2 delta = add2_rn(mb, make_float2(-s1[h].x, -s1[h].y));
+            s1[h] = fma2_rn(delta, make_float2(share, share), s1[h]);
+            sq = fma2_rn(mul2_rn(delta, delta), make_float2(cross, cross), sq);
+            s2[h] = add2_rn(s2[h], sq);
+          }
         }
       }
-      float t1[V], t2[V];  // sums of the batch join the running ones once
+      n += ALL ? K : nb;
+    };
+    int slot = 0;
+    for (int i = 0; i < chunks - 1; ++i) {
+      arrive_full(slot);
+      if (live) reduce(norm_smem + slot * slot_bytes + offset, K, std::true_type{});
+      if (i + NS < chunks) release(slot);  // the last chunks stay for the second pass
+      slot = slot + 1 == NS ? 0 : slot + 1;
+    }
+    // this thread's rows of the last chunk
+    const int last_left = hi - lo - (chunks - 1) * chunk_rows - row;
+    const int last_have = live && last_left > 0 ? (last_left + p.rpi - 1) / p.rpi : 0;
+    const int last_nb = last_have < K ? last_have : K;
+    arrive_full(slot);
+    if (last_nb == K)
+      reduce(norm_smem + slot * slot_bytes + offset, K, std::true_type{});
+    else if (last_nb > 0)
+      reduce(norm_smem + slot * slot_bytes + offset, last_nb, std::false_type{});
+
+    // ---- the slab's groups.  A thread first joins runs of `run` channels of
+    // its vector that share a group; region[row][vec * (V / run) + i].
+    const int run = p.run, per = V / run;   // 1, 2, 4 or 8 channels
+    const int width = p.tpr * per;          // entries of a row
+    const int cpg = c / run;                // entries of a group in a row
+    const int pixels = hi - lo;
+    named_barrier_sync(kNormBar, kNormThreads);  // the region is free again
+    if (live) {
+      float a[V], d[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) t1[i] = t2[i] = 0.0f;
+      for (int h = 0; h < H; ++h) {
+        a[2 * h] = s1[h].x; a[2 * h + 1] = s1[h].y;
+        d[2 * h] = s2[h].x; d[2 * h + 1] = s2[h].y;
+      }
+      if constexpr (BWD) {
+        // the rows' sums: region [rpi][C]
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        if (s0 + j * p.rpi >= hi) break;
+        for (int i = 0; i < V; ++i) region[row * p.C + vec * V + i] = make_float2(a[i], d[i]);
+      } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float xh = (to_f32<T>(xv[j][i]) - mean[i]) * rstd[i];
-          float dz = to_f32<T>(gv[j][i]);
-          if (p.silu) dz *= silu_grad(__fmaf_rn(xh, w[i], bias[i]));
-          t1[i] += dz;
-          t2[i] = __fmaf_rn(dz, xh, t2[i]);
+        for (int w = 1; w < V; w *= 2) {     // equal counts: mean of means
+          if (w < run) {
+            const float nw = 0.5f * n * w;
+#pragma unroll
+            for (int i = 0; i < V; i += 2 * w) {
+              const float delta = a[i + w] - a[i];
+              a[i] += 0.5f * delta;
+              d[i] += d[i + w] + delta * delta * nw;
+            }
+          }
+        }
+        if (run == 1) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) region[row * width + vec * V + i] = make_float2(a[i], d[i]);
+        } else if (run == 2) {
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) region[row * width + vec * (V / 2) + i] = make_float2(a[2 * i], d[2 * i]);
+        } else if (run == 4) {
+#pragma unroll
+          for (int i = 0; i < V / 4; ++i) region[row * width + vec * (V / 4) + i] = make_float2(a[4 * i], d[4 * i]);
+        } else {
+          region[row * width + vec] = make_float2(a[0], d[0]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        s1[i] += t1[i];
-        s2[i] += t2[i];
+    }
+    named_barrier_sync(kNormBar, kNormThreads);
+    if constexpr (BWD) {
+      // per channel over the rows, to global memory; weighted in place
+      for (int ch = tid; ch < p.C; ch += kNormThreads) {
+        float2 t = region[ch];
+        for (int r = 1; r < p.rpi; ++r) {
+          t.x += region[r * p.C + ch].x;
+          t.y += region[r * p.C + ch].y;
+        }
+        if (ok) p.chan[(static_cast<int64_t>(b) * p.slabs + slab) * p.C + ch] = t;
+        float w = 1.0f;
+        if (p.weight != nullptr)
+          w = p.param_f32 ? __ldg(static_cast<const float *>(p.weight) + ch)
+                          : to_f32<T>(static_cast<const T *>(p.weight)[ch]);
+        region[ch] = make_float2(w * t.x, w * t.y);
+      }
+      named_barrier_sync(kNormBar, kNormThreads);
+    }
+    // `lanes` neighbouring threads per group join its entries, publish them
+    // or (alone) finish the group.  All groups at once up to 512 of them.
+    float2 *stat = region + (BWD ? p.C : p.rpi * width);
+    const float count = static_cast<float>(p.S) * c;  // values of a group
+    uint4 *const entries = p.entries + static_cast<int64_t>(b) * p.G * p.slabs;
+    const int lanes = p.group_lanes, sub = tid & (lanes - 1);
+    auto group_sum = [&](float v) {
+      for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      return v;
+    };
+    auto finish = [&](float2 t) {
+      return BWD ? make_float2(t.x / count, t.y / count) : make_float2(t.x, rsqrtf(t.y / count + p.eps));
+    };
+    const int gstep = kNormThreads / lanes;
+    for (int g0 = 0; g0 < p.G; g0 += gstep) {  // whole warps stay together
+      const int g = g0 + tid / lanes;
+      float2 mine = make_float2(0.0f, 0.0f);
+      if constexpr (BWD) {
+        if (g < p.G) {
+          for (int e = sub; e < c; e += lanes) {
+            mine.x += region[g * c + e].x;
+            mine.y += region[g * c + e].y;
+          }
+        }
+        mine = make_float2(group_sum(mine.x), group_sum(mine.y));
+      } else {
+        // entry e: `run` channels of the group in row e / cpg, standing for
+        // the row's pixels.  Rows below pixels % rpi have one pixel more.
+        const int many = pixels / p.rpi, more = pixels - many * p.rpi;
+        const int total = p.rpi * cpg;
+        const float2 *from = region + g * cpg;
+        if (g < p.G) {
+          int r = sub / cpg, col = sub - r * cpg;
+          for (int e = sub; e < total; e += lanes) {
+            mine.x += static_cast<float>(many + (r < more ? 1 : 0)) * from[r * width + col].x;
+            for (col += lanes; col >= cpg; col -= cpg) ++r;
+          }
+        }
+        const float mean = group_sum(mine.x) / (static_cast<float>(pixels) * cpg);
+        if (g < p.G) {
+          int r = sub / cpg, col = sub - r * cpg;
+          for (int e = sub; e < total; e += lanes) {
+            const float2 st = from[r * width + col];
+            const float dd = st.x - mean;
+            mine.y += st.y + static_cast<float>(many + (r < more ? 1 : 0)) * run * dd * dd;
+            for (col += lanes; col >= cpg; col -= cpg) ++r;
+          }
+        }
+        mine = make_float2(mean, group_sum(mine.y));
+      }
+      if (sub == 0 && g < p.G) {
+        if (p.slabs == 1) stat[g] = finish(mine);
+        else if (ok) entry_store(entries + static_cast<int64_t>(g) * p.slabs + slab, mine, p.tag);
       }
     }
+    // what the second pass needs of the parameters, while the entries travel
+    float2 wt2[H], bs2[H];
+    if constexpr (!BWD) {
+      if (live) {
+        norm_param<T>(p.weight, p.param_f32, vec * V, 1.0f, wt2);
+        norm_param<T>(p.bias, p.param_f32, vec * V, 0.0f, bs2);
+      }
+    }
+    // ---- the sample's groups, from every block's entry
+    if (p.slabs > 1) {
+      constexpr int E = 10;  // entries a lane keeps in registers
+      const int part = p.S / p.slabs, extra = p.S - part * p.slabs;
+      for (int g0 = 0; g0 < p.G; g0 += gstep) {
+        const int g = g0 + tid / lanes;
+        const uint4 *e = entries + static_cast<int64_t>(g) * p.slabs;
+        float2 v[E], t = make_float2(0.0f, 0.0f);
+        if (p.slabs <= E * lanes) {
+          unsigned long long tag[E];
 #pragma unroll
-    for (int i = 0; i < V; ++i) chan_sum[row * p.C + vec * V + i] = make_float2(s1[i], s2[i]);
-  }
-  __syncthreads();
-  const int64_t slot = static_cast<int64_t>(b) * p.slabs + slab;
-  for (int ch = threadIdx.x; ch < p.C; ch += blockDim.x) {
-    float2 t = chan_sum[ch];
-    for (int r = 1; r < p.rpi; ++r) {
-      t.x += chan_sum[r * p.C + ch].x;
-      t.y += chan_sum[r * p.C + ch].y;
+          for (int u = 0; u < E; ++u) {  // all loads under way at once
+            const int j = sub + lanes * u;
+            tag[u] = p.tag;
+            v[u] = make_float2(0.0f, 0.0f);
+            if (j < p.slabs && g < p.G) tag[u] = entry_load(e + j, v[u]);
+          }
+#pragma unroll
+          for (int u = 0; u < E; ++u) {
+            if (tag[u] != p.tag && ok) ok = entry_wait(e + sub + lanes * u, p.tag, v[u], &abort_flag);
+          }
+#pragma unroll
+          for (int u = 0; u < E; ++u) {
+            const int j = sub + lanes * u;
+            const float pix = j < p.slabs ? static_cast<float>(part + (j < extra ? 1 : 0)) : 0.0f;
+            t.x += BWD ? v[u].x : pix * v[u].x;
+            if (BWD) t.y += v[u].y;
+          }
+          t.x = group_sum(t.x);
+          if constexpr (!BWD) {
+            t.x /= static_cast<float>(p.S);
+#pragma unroll
+            for (int u = 0; u < E; ++u) {
+              const int j = sub + lanes * u;
+              const float pix = j < p.slabs ? static_cast<float>(part + (j < extra ? 1 : 0)) : 0.0f;
+              const float dd = v[u].x - t.x;
+              t.y += v[u].y + pix * c * dd * dd;
+            }
+          }
+          t.y = group_sum(t.y);
+        } else {  // many groups: the entries are read twice
+          if (g < p.G) {
+            for (int j = sub; j < p.slabs && ok; j += lanes) {
+              ok = entry_wait(e + j, p.tag, v[0], &abort_flag);
+              t.x += BWD ? v[0].x : static_cast<float>(part + (j < extra ? 1 : 0)) * v[0].x;
+              if (BWD) t.y += v[0].y;
+            }
+          }
+          t.x = group_sum(t.x);
+          if constexpr (!BWD) {
+            t.x /= static_cast<float>(p.S);
+            if (g < p.G) {
+              for (int j = sub; j < p.slabs && ok; j += lanes) {
+                entry_load(e + j, v[0]);
+                const float dd = v[0].x - t.x;
+                t.y += v[0].y + static_cast<float>(part + (j < extra ? 1 : 0)) * c * dd * dd;
+              }
+            }
+          }
+          t.y = group_sum(t.y);
+        }
+        if (sub == 0 && g < p.G) stat[g] = finish(t);
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok);
     }
-    p.chan[slot * p.C + ch] = t;
-    const float w = norm_param(p.weight, p.param_f32, ch, 1.0f, static_cast<const T *>(nullptr));
-    chan_sum[ch] = make_float2(w * t.x, w * t.y);  // this thread's own entries
-  }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  for (int g = warp; g < p.G; g += warps) {
-    float a = 0.0f, d = 0.0f;
-    for (int i = lane; i < c; i += 32) {
-      a += chan_sum[g * c + i].x;
-      d += chan_sum[g * c + i].y;
+    named_barrier_sync(kNormBar, kNormThreads);
+    if (p.slabs > 1 && tid == 0 && ok) {  // this block has read the sample's entries
+      __threadfence();
+      *reinterpret_cast<volatile unsigned long long *>(p.readers + static_cast<int64_t>(b) * p.slabs + slab) = p.tag;
     }
-    a = warp_sum(a);
-    d = warp_sum(d);
-    if (lane == 0) p.part[slot * p.G + g] = make_float2(a, d);
+    if (!BWD && slab == 0 && p.mean_out != nullptr && ok) {
+      for (int g = tid; g < p.G; g += kNormThreads) {
+        p.mean_out[static_cast<int64_t>(b) * p.G + g] = stat[g].x;
+        p.rstd_out[static_cast<int64_t>(b) * p.G + g] = stat[g].y;
+      }
+    }
+
+    // ---- second pass, backwards
+    // forward: y = act((x + k3) * k1 + k2); gradient: dx = dz * k1 + k2 + xh * k3
+    float2 k1[H], k2[H], k3[H];
+    if (live) {
+      each_group<V>(vec * V, c, [&](int i, int g) {
+        const float2 st = stat[g];
+        if constexpr (BWD) {
+          const float r = at(rs, i);
+          at(k1, i) = r * at(wt, i);
+          at(k2, i) = -r * st.x;
+          at(k3, i) = -r * st.y;
+        } else {
+          at(k1, i) = st.y * at(wt2, i);
+          at(k2, i) = at(bs2, i);
+          at(k3, i) = -st.x;
+        }
+      });
+    }
+    uint32_t *row_max = reinterpret_cast<uint32_t *>(stat + p.G);  // int8 form: [3][chunk_rows]
+    if constexpr (MODE == kNormQuant) {
+      for (int i = tid; i < 3 * chunk_rows; i += kNormThreads) row_max[i] = 0u;
+      named_barrier_sync(kNormBar, kNormThreads);
+    }
+    int turn = 0;
+    const bool one_row = (p.tpr & 31) == 0;        // a warp's threads share a row
+    const int first = __shfl_sync(0xFFFFFFFFu, row, 0);
+    for (int i = chunks - 1; i >= 0; --i) {
+      const int r0 = lo + i * chunk_rows;
+      const int nb = i == chunks - 1 ? last_nb : (live ? K : 0);
+      if (i < chunks - NS) arrive_full(slot);
+      const uint8_t *src = norm_smem + slot * slot_bytes + offset;
+      if constexpr (MODE == kNormQuant) {
+        static_assert(V == 8 || MODE != kNormQuant, "int8 rows are made of bf16 activations");
+        uint32_t *mx = row_max + turn * chunk_rows;
+        float2 z[K][H];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          float m = 0.0f;
+          if (k < nb) {
+            Pairs<T>::get(*reinterpret_cast<const uint4 *>(src + k * row_step), z[k]);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              z[k][h] = fma2_rn(add2_rn(z[k][h], k3[h]), k1[h], k2[h]);
+              if (p.silu) z[k][h] = mul2_rn(z[k][h], sigmoid2(z[k][h]));
+              m = fmaxf(m, fmaxf(fabsf(z[k][h].x), fabsf(z[k][h].y)));
+            }
+          }
+          // A row's threads are neighbours: a warp holds one or two rows, or,
+          // of narrow rows, several.  One maximum per warp and row goes to
+          // shared memory (maxima do not depend on the order).
+          const uint32_t mb = __float_as_uint(m);
+          if (one_row) {
+            const uint32_t m0 = __reduce_max_sync(0xFFFFFFFFu, mb);
+            if (lane == 0 && k < nb) atomicMax(mx + row + k * p.rpi, m0);
+          } else if (p.tpr > 32) {
+            const uint32_t m0 = __reduce_max_sync(0xFFFFFFFFu, row == first ? mb : 0u);
+            const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, row == first ? 0u : mb);
+            if (lane == 0) {
+              if (first < p.rpi) atomicMax(mx + first + k * p.rpi, m0);
+              if (first + 1 < p.rpi) atomicMax(mx + first + 1 + k * p.rpi, m1);
+            }
+          } else if (k < nb) {
+            atomicMax(mx + row + k * p.rpi, mb);
+          }
+        }
+        named_barrier_sync(kNormBar, kNormThreads);
+        // the maxima of two chunks ago are no longer read: clear them for the
+        // chunk after the next
+        uint32_t *old = row_max + (turn == 0 ? 2 : turn - 1) * chunk_rows;
+        for (int r = tid; r < chunk_rows; r += kNormThreads) old[r] = 0u;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (k < nb && ok) {
+            const float amax = __uint_as_float(mx[row + k * p.rpi]);
+            // rint(y * (127 / amax)) in one fused step: y is a rounded fp32
+            // value already, so a quotient off by 2^-22 moves a code only
+            // where y is that close to a tie; the scale is the IEEE quotient.
+            // Next to the subnormals, where 127 / amax leaves fp32, divide.
+            uint32_t code[V];
+            if (amax >= 1e-30f) {
+              const float r = __fdividef(127.0f, amax);
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                const float2 t = fma2_rn(z[k][h], make_float2(r, r), make_float2(kRintMagic, kRintMagic));
+                code[2 * h] = __float_as_uint(t.x);
+                code[2 * h + 1] = __float_as_uint(t.y);
+              }
+            } else {
+              const float sc = __fdiv_rn(amax, 127.0f);
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                code[2 * h] = sc == 0.0f ? 0u : quant_exact(z[k][h].x, sc);
+                code[2 * h + 1] = sc == 0.0f ? 0u : quant_exact(z[k][h].y, sc);
+              }
+            }
+            const int64_t pix = static_cast<int64_t>(b) * p.S + r0 + row + k * p.rpi;
+            *reinterpret_cast<uint2 *>(p.q + pix * p.C + vec * V) = pack_codes(code);
+            if (vec == 0) p.s_q[pix] = __fdiv_rn(amax, 127.0f);
+          }
+        }
+        turn = turn == 2 ? 0 : turn + 1;
+      } else {
+        uint8_t *dst = static_cast<uint8_t *>(p.y) +
+                       (b * p.yb + (r0 + row) * p.ys + vec * V) * static_cast<int64_t>(sizeof(T));
+        const int64_t dst_step = p.rpi * p.ys * static_cast<int64_t>(sizeof(T));
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (k < nb && ok) {
+            float2 z[H];
+            if constexpr (BWD) {
+              float2 xh[H];
+              grad_vec(*reinterpret_cast<const uint4 *>(src + k * row_step),
+                       *reinterpret_cast<const uint4 *>(src + p.chunk_bytes + k * row_step), xh, z);
+#pragma unroll
+              for (int h = 0; h < H; ++h)
+                z[h] = fma2_rn(z[h], k1[h], fma2_rn(xh[h], k3[h], k2[h]));
+            } else {
+              Pairs<T>::get(*reinterpret_cast<const uint4 *>(src + k * row_step), z);
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                z[h] = fma2_rn(add2_rn(z[h], k3[h]), k1[h], k2[h]);
+                if (p.silu) z[h] = mul2_rn(z[h], sigmoid2(z[h]));
+              }
+            }
+            *reinterpret_cast<uint4 *>(dst + k * dst_step) = Pairs<T>::put(z);
+          }
+        }
+      }
+      release(slot);
+      slot = slot == 0 ? NS - 1 : slot - 1;
+    }
   }
 }
 
 // dw and db: one warp per channel adds the slabs' sums in a fixed order.
-__global__ void __launch_bounds__(256) norm_grad_params_kernel(const NormParams p) {
+__global__ void __launch_bounds__(256) norm_grad_params_kernel(const __grid_constant__ NormParams p) {
   const int ch = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (ch >= p.C) return;
   float a = 0.0f, d = 0.0f;
@@ -406,74 +837,6 @@ __global__ void __launch_bounds__(256) norm_grad_params_kernel(const NormParams 
   if (lane == 0) {
     if (p.dbias != nullptr) p.dbias[ch] = a;
     if (p.dweight != nullptr) p.dweight[ch] = d;
-  }
-}
-
-// dx of one slab.
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_apply_kernel(const NormParams p) {
-  constexpr int V = kNormVec<T>;
-  constexpr int R = 4;
-  extern __shared__ float2 group_sum[];  // [G]: (1/n) sum w dz, (1/n) sum w dz xh
-  const int b = blockIdx.x / p.slabs, slab = blockIdx.x - b * p.slabs;
-  int lo, hi;
-  slab_range(p.S, p.slabs, slab, lo, hi);
-  const int c = p.C / p.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  {
-    const float inv_n = 1.0f / (static_cast<float>(p.S) * c);
-    for (int g = warp; g < p.G; g += warps) {
-      float a = 0.0f, d = 0.0f;
-      for (int j = lane; j < p.slabs; j += 32) {
-        const float2 t = p.part[(static_cast<int64_t>(b) * p.slabs + j) * p.G + g];
-        a += t.x;
-        d += t.y;
-      }
-      a = warp_sum(a);
-      d = warp_sum(d);
-      if (lane == 0) group_sum[g] = make_float2(a * inv_n, d * inv_n);
-    }
-  }
-  __syncthreads();
-  const int row = threadIdx.x / p.tpr, vec = threadIdx.x - row * p.tpr;
-  if (row >= p.rpi) return;
-  float mean[V], rstd[V], w[V], bias[V], c1[V], c2[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int ch = vec * V + i;
-    mean[i] = p.mean_in[static_cast<int64_t>(b) * p.G + ch / c];
-    rstd[i] = p.rstd_in[static_cast<int64_t>(b) * p.G + ch / c];
-    w[i] = norm_param(p.weight, p.param_f32, ch, 1.0f, static_cast<const T *>(nullptr));
-    bias[i] = norm_param(p.bias, p.param_f32, ch, 0.0f, static_cast<const T *>(nullptr));
-    c1[i] = group_sum[ch / c].x;
-    c2[i] = group_sum[ch / c].y;
-  }
-  const T *x = static_cast<const T *>(p.x) + b * p.xb + vec * V;
-  const T *dy = static_cast<const T *>(p.dy) + b * p.dyb + vec * V;
-  T *dx = static_cast<T *>(p.y) + b * p.yb + vec * V;
-  for (int s0 = lo + row; s0 < hi; s0 += R * p.rpi) {
-    T xv[R][V], gv[R][V];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int s = s0 + j * p.rpi;
-      if (s < hi) {
-        VecIO<T, V, true>::load(x + s * p.xs, xv[j]);
-        VecIO<T, V, true>::load(dy + s * p.dys, gv[j]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int s = s0 + j * p.rpi;
-      if (s >= hi) break;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float xh = (to_f32<T>(xv[j][i]) - mean[i]) * rstd[i];
-        float dz = to_f32<T>(gv[j][i]);
-        if (p.silu) dz *= silu_grad(__fmaf_rn(xh, w[i], bias[i]));
-        gv[j][i] = from_f32<T>(rstd[i] * (__fmaf_rn(w[i], dz, -c1[i]) - xh * c2[i]));
-      }
-      VecIO<T, V, true>::store(dx + s * p.ys, gv[j]);
-    }
   }
 }
 
