@@ -146,7 +146,7 @@ def test_rotary_far_positions_and_a_shared_row_of_them():
     x = torch.randn((3, len(pos), 2, 64), generator=gen(5))
     y = w8a8.rotary(x.cuda(), pos.cuda(), freq, layout="half")  # [tokens], shared by the batch
     # exact turns in whole numbers
-    turns = torch.tensor([[p * int(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 / 2.0 ** 64 for f in freq.tolist()]
+    turns = torch.tensor([[p * int(f * (2.0 ** 64 / (2 * math.pi))) % 2 ** 64 / 2.0 ** 64 for f in freq.tolist()]
                           for p in pos.tolist()], dtype=torch.float64) * (2 * math.pi)
     c, s = turns.cos()[None, :, None], turns.sin()[None, :, None]
     a, b = x[..., :32].double(), x[..., 32:].double()

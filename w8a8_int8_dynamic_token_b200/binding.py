@@ -574,8 +574,20 @@ def _scratch(need, workspace, dev):
     `need` bytes (allocated on the launching stream, inside _launching; kept
     alive by the caller until the launches have been enqueued)."""
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), need
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _handle(s) -> int:
+    """The raw handle of what _launching yields."""
+    return s if isinstance(s, int) else s.cuda_stream
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def linear_input_grad(dy, Wq, s_w, out=None, workspace=None, variant=VARIANT_AUTO, stream=None):
@@ -597,9 +609,9 @@ def linear_input_grad(dy, Wq, s_w, out=None, workspace=None, variant=VARIANT_AUT
     with _launching(dev, stream) as s:
         dx = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
         ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
-        _check(w8a8_linear_input_grad(_ptr(dy), M, N, dy.stride(0), _ptr(Wq), _ptr(s_w), K,
-                                      _ptr(dx), dx.stride(0), variant, ws_ptr, ws_bytes,
-                                      _stream(s)), "w8a8_linear_input_grad")
+        _check(w8a8_linear_input_grad(dy.data_ptr(), M, N, dy.stride(0), Wq.data_ptr(),
+                                      s_w.data_ptr(), K, dx.data_ptr(), dx.stride(0), variant,
+                                      ws_ptr, ws_bytes, _handle(s)), "w8a8_linear_input_grad")
         del ws
     return dx
 
@@ -652,19 +664,30 @@ def _heads(t, name, dtype):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
-    if t.dim() not in (3, 4):
+
+
+@functools.lru_cache(maxsize=4096)
+def _head_strides(shape, strides, name):
+    """(batch, tokens, heads, dim) and the strides of the first three."""
+    if len(shape) not in (3, 4):
         raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
-    if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if shape[-1] > 1 and strides[-1] != 1 and 0 not in shape:
         raise ValueError(f"{name} must have unit stride in its last dimension")
+    four = len(shape) == 4
+    return (shape[0] if four else 1, *shape[-3:]), (strides[0] if four else 0, *strides[-3:-1])
 
 
-def _rotary_heads(entry, x, y):
-    four = x.dim() == 4
-    xs, ys = x.stride(), y.stride()
-    entry.x, entry.y, entry.heads = x.data_ptr(), y.data_ptr(), x.shape[-2]
-    entry.x_batch, entry.y_batch = (xs[0], ys[0]) if four else (0, 0)
-    entry.x_token, entry.x_head = xs[-3], xs[-2]
-    entry.y_token, entry.y_head = ys[-3], ys[-2]
+@functools.lru_cache(maxsize=4096)
+def _position_strides(shape, strides, batch, tokens, with_axes):
+    """(batch stride, token stride, axes) of positions."""
+    lead = len(shape) - with_axes
+    if lead not in (1, 2) or shape[lead - 1] != tokens or (lead == 2 and shape[0] != batch):
+        raise ValueError(f"positions must be [{tokens}] or [{batch}, {tokens}]"
+                         + (" and a last dimension of axes" if with_axes else ""))
+    axes = shape[-1] if with_axes else 1
+    if axes > 1 and strides[-1] != 1:
+        raise ValueError("positions must have unit stride in its last dimension")
+    return strides[0] if lead == 2 else 0, strides[lead - 1], axes
 
 
 def rotary(x, positions, inv_freq, k=None, layout="interleaved", axis=None, scale=1.0,
@@ -677,62 +700,55 @@ def rotary(x, positions, inv_freq, k=None, layout="interleaved", axis=None, scal
     [tokens] or [batch, tokens], or with a last dimension of axes when `axis`
     (CPU int32 [rot / 2], the axis of each pair) is given.  backward=True: the
     gradient.  out / out_k: where to write; x / k themselves, or memory that
-    does not overlap them.  Returns y, or (y, y_k) with k."""
+    does not overlap them.  Returns y, or (y, y_k) with k, laid out as x and k
+    where those are dense."""
     _heads(x, "x", None)
+    dtype = x.dtype
+    (batch, tokens, heads, dim), (xb, xt, xh) = _head_strides(x.shape, x.stride(), "x")
     if layout not in _LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or \
             inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a dense 1-D CPU float64 tensor")
-    rot, dim = 2 * inv_freq.shape[0], x.shape[-1]
+    rot = 2 * inv_freq.shape[0]
     if rot > dim:
         raise ValueError(f"inv_freq turns {rot} values of a head, which has {dim}")
     if out is not None:
-        _heads(out, "out", x.dtype)
+        _heads(out, "out", dtype)
         _shape(out, "out", x.shape)
     if k is not None:
-        _heads(k, "k", x.dtype)
-        if k.dim() != x.dim() or k.shape[:-2] != x.shape[:-2] or k.shape[-1] != dim:
+        _heads(k, "k", dtype)
+        (kb_, kt_, k_heads, kd_), (kb, kt, kh) = _head_strides(k.shape, k.stride(), "k")
+        if k.dim() != x.dim() or (kb_, kt_, kd_) != (batch, tokens, dim):
             raise ValueError("x and k differ in more than their heads")
         if out_k is not None:
-            _heads(out_k, "out_k", x.dtype)
+            _heads(out_k, "out_k", dtype)
             _shape(out_k, "out_k", k.shape)
     elif out_k is not None:
         raise ValueError("out_k is given without k")
     if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
         raise TypeError("positions must be an int32 or int64 tensor")
-    batch, tokens = (x.shape[0] if x.dim() == 4 else 1), x.shape[-3]
-    lead = positions.dim()
-    axes = 1
-    if axis is not None:
-        if not isinstance(axis, torch.Tensor) or axis.dtype != torch.int32 or axis.is_cuda or \
-                tuple(axis.shape) != tuple(inv_freq.shape) or not axis.is_contiguous():
-            raise TypeError("axis must be a dense CPU int32 tensor of inv_freq's shape")
-        lead -= 1
-        if lead not in (1, 2):
-            raise ValueError("positions must end in a dimension of axes when axis is given")
-        axes = positions.shape[-1]
-        if axes > 1 and positions.stride(-1) != 1:
-            raise ValueError("positions must have unit stride in its last dimension")
-    if lead not in (1, 2) or positions.shape[lead - 1] != tokens or \
-            (lead == 2 and positions.shape[0] != batch):
-        raise ValueError(f"positions must be [{tokens}] or [{batch}, {tokens}]"
-                         + (" and axes" if axis is not None else ""))
+    if axis is not None and (
+            not isinstance(axis, torch.Tensor) or axis.dtype != torch.int32 or axis.is_cuda or
+            axis.shape != inv_freq.shape or not axis.is_contiguous()):
+        raise TypeError("axis must be a dense CPU int32 tensor of inv_freq's shape")
+    pos_b, pos_t, axes = _position_strides(positions.shape, positions.stride(), batch, tokens,
+                                           axis is not None)
     dev = _on_one_device(x=x, k=k, positions=positions, out=out, out_k=out_k)
-    ps = positions.stride()
     with _launching(dev, stream) as s:
-        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=dev)
-        entries = (RotaryHeads * 2)()
-        _rotary_heads(entries[0], x, y)
+        y = out if out is not None else torch.empty_like(x)
+        _, (yb, yt, yh) = _head_strides(y.shape, y.stride(), "out")
+        tensors = (RotaryHeads * 2)((x.data_ptr(), y.data_ptr(), heads, xb, xt, xh, yb, yt, yh))
         y_k = None
         if k is not None:
-            y_k = out_k if out_k is not None else torch.empty(k.shape, dtype=x.dtype, device=dev)
-            _rotary_heads(entries[1], k, y_k)
-        _check(w8a8_rotary(entries, 1 if k is None else 2, _DTYPES[x.dtype], batch, tokens, dim, rot,
-                           _LAYOUTS[layout], positions.data_ptr(), 8 * positions.element_size(),
-                           ps[0] if lead == 2 else 0, ps[lead - 1], axes, inv_freq.data_ptr(),
-                           None if axis is None else axis.data_ptr(), scale, int(bool(backward)),
-                           _stream(s)), "w8a8_rotary")
+            y_k = out_k if out_k is not None else torch.empty_like(k)
+            _, (yb, yt, yh) = _head_strides(y_k.shape, y_k.stride(), "out_k")
+            tensors[1] = (k.data_ptr(), y_k.data_ptr(), k_heads, kb, kt, kh, yb, yt, yh)
+        _check(w8a8_rotary(tensors, 1 if k is None else 2, _DTYPES[dtype], batch, tokens, dim, rot,
+                           _LAYOUTS[layout], positions.data_ptr(),
+                           64 if positions.dtype == torch.int64 else 32, pos_b, pos_t, axes,
+                           inv_freq.data_ptr(), _address(axis), scale, 1 if backward else 0,
+                           _handle(s)), "w8a8_rotary")
     return y if k is None else (y, y_k)
 
 
@@ -744,23 +760,22 @@ def group_norm_workspace_size(B: int, S: int, C: int, groups: int, dtype=torch.b
     return n
 
 
-def _pixels(t, name, shape=None, dtype=None):
-    """Channels-last [B, ..., C]: (B, pixels, C, sample stride, pixel stride).
-    The dimensions between must be evenly strided, as one run of pixels."""
+def _channels_last(t, name, dtype=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
-    if t.dim() < 3:
+
+
+@functools.lru_cache(maxsize=4096)
+def _pixels(sizes, strides, name):
+    """Channels-last [B, ..., C]: (B, pixels, C, sample stride, pixel stride).
+    The dimensions between must be evenly strided, as one run of pixels."""
+    if len(sizes) < 3:
         raise ValueError(f"{name} must be [B, ..., C] with its channels last")
-    if shape is not None:
-        _shape(t, name, shape)
-    sizes, strides = t.shape, t.stride()
     if sizes[-1] > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    if t.dim() == 3:
-        return sizes[0], sizes[1], sizes[2], strides[0], strides[1]
-    pixels, step = 1, 0
+    pixels, step = 1, sizes[-1]
     for n, st in zip(reversed(sizes[1:-1]), reversed(strides[1:-1])):
         if n == 1:
             continue
@@ -769,7 +784,7 @@ def _pixels(t, name, shape=None, dtype=None):
         elif st != step * pixels:
             raise ValueError(f"{name}'s pixels must be evenly strided")
         pixels *= n
-    return sizes[0], pixels, sizes[-1], strides[0], step or sizes[-1]
+    return sizes[0], pixels, sizes[-1], strides[0], step
 
 
 def _norm_params(x, C, weight, bias):
@@ -778,9 +793,9 @@ def _norm_params(x, C, weight, bias):
     for name, t in (("weight", weight), ("bias", bias)):
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or t.dtype not in (x.dtype, torch.float32):
+        if not isinstance(t, torch.Tensor) or (t.dtype != x.dtype and t.dtype != torch.float32):
             raise TypeError(f"{name} must be a {x.dtype} or float32 tensor")
-        if tuple(t.shape) != (C,) or not t.is_contiguous():
+        if t.shape != (C,) or not t.is_contiguous():
             raise ValueError(f"{name} must be a dense [{C}] tensor")
         dtype = t.dtype
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
@@ -800,24 +815,28 @@ def group_norm(x, groups, weight=None, bias=None, eps=1e-5, activation=None, out
     with an optional SiLU: y in x's type and shape (and, with return_stats, the
     mean and 1 / standard deviation, fp32 [B, groups], that the backward pass
     takes).  out may be x itself."""
-    B, S, C, xb, xs = _pixels(x, "x")
+    _channels_last(x, "x")
+    B, S, C, xb, xs = _pixels(x.shape, x.stride(), "x")
     act = _activation(activation)
     pdt = _norm_params(x, C, weight, bias)
     if out is not None:
-        _, _, _, yb, ys = _pixels(out, "out", x.shape, x.dtype)
+        _channels_last(out, "out", x.dtype)
+        _shape(out, "out", x.shape)
     dev = _on_one_device(x=x, weight=weight, bias=bias, out=out, workspace=workspace)
     need = group_norm_workspace_size(B, S, C, groups, x.dtype)
     with _launching(dev, stream) as s:
         y = out
         if y is None:
-            y, yb, ys = torch.empty(x.shape, dtype=x.dtype, device=dev), S * C, C
+            y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        _, _, _, yb, ys = _pixels(y.shape, y.stride(), "out")
         mean = rstd = None
         if return_stats:
             mean, rstd = torch.empty((2, B, groups), dtype=torch.float32, device=dev).unbind()
         ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
-        _check(w8a8_group_norm(_ptr(x), xb, xs, _DTYPES[x.dtype], B, S, C, groups, _ptr(weight),
-                               _ptr(bias), pdt, eps, act, _ptr(y), yb, ys, _ptr(mean), _ptr(rstd),
-                               ws_ptr, ws_bytes, _stream(s)), "w8a8_group_norm")
+        _check(w8a8_group_norm(x.data_ptr(), xb, xs, _DTYPES[x.dtype], B, S, C, groups,
+                               _address(weight), _address(bias), pdt, eps, act, y.data_ptr(), yb,
+                               ys, _address(mean), _address(rstd), ws_ptr, ws_bytes, _handle(s)),
+               "w8a8_group_norm")
         del ws
     return (y, mean, rstd) if return_stats else y
 
@@ -827,21 +846,23 @@ def group_norm_quant(x, groups, weight=None, bias=None, eps=1e-5, activation=Non
     """group_norm of a bf16 x as the operand of linear(): (q int8 [B * pixels,
     C], s_a fp32 [B * pixels]), the rows of the fp32 result quantized per pixel
     (and the statistics, with return_stats)."""
-    B, S, C, xb, xs = _pixels(x, "x", None, torch.bfloat16)
+    _channels_last(x, "x", torch.bfloat16)
+    B, S, C, xb, xs = _pixels(x.shape, x.stride(), "x")
     act = _activation(activation)
     pdt = _norm_params(x, C, weight, bias)
     dev = _on_one_device(x=x, weight=weight, bias=bias, workspace=workspace)
     need = group_norm_workspace_size(B, S, C, groups, x.dtype)
     with _launching(dev, stream) as s:
         q = torch.empty((B * S, C), dtype=torch.int8, device=dev)
-        s_a = torch.empty((B * S,), dtype=torch.float32, device=dev)
+        s_a = torch.empty(B * S, dtype=torch.float32, device=dev)
         mean = rstd = None
         if return_stats:
             mean, rstd = torch.empty((2, B, groups), dtype=torch.float32, device=dev).unbind()
         ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
-        _check(w8a8_group_norm_quant(_ptr(x), xb, xs, B, S, C, groups, _ptr(weight), _ptr(bias),
-                                     pdt, eps, act, _ptr(q), _ptr(s_a), _ptr(mean), _ptr(rstd),
-                                     ws_ptr, ws_bytes, _stream(s)), "w8a8_group_norm_quant")
+        _check(w8a8_group_norm_quant(x.data_ptr(), xb, xs, B, S, C, groups, _address(weight),
+                                     _address(bias), pdt, eps, act, q.data_ptr(), s_a.data_ptr(),
+                                     _address(mean), _address(rstd), ws_ptr, ws_bytes, _handle(s)),
+               "w8a8_group_norm_quant")
         del ws
     return (q, s_a, mean, rstd) if return_stats else (q, s_a)
 
@@ -852,8 +873,11 @@ def group_norm_backward(dy, x, mean, rstd, weight=None, bias=None, activation=No
     group_norm_quant): (dx in x's type, dweight, dbias fp32 [C], None where
     there is no such parameter).  mean, rstd: the forward's statistics; out may
     be dy or x itself."""
-    B, S, C, xb, xs = _pixels(x, "x")
-    _, _, _, gb, gs = _pixels(dy, "dy", x.shape, x.dtype)
+    _channels_last(x, "x")
+    B, S, C, xb, xs = _pixels(x.shape, x.stride(), "x")
+    _channels_last(dy, "dy", x.dtype)
+    _shape(dy, "dy", x.shape)
+    _, _, _, gb, gs = _pixels(dy.shape, dy.stride(), "dy")
     act = _activation(activation)
     pdt = _norm_params(x, C, weight, bias)
     _need(mean, "mean", torch.float32, 2)
@@ -864,21 +888,24 @@ def group_norm_backward(dy, x, mean, rstd, weight=None, bias=None, activation=No
         if not t.is_contiguous():
             raise ValueError(f"{name} must be dense")
     if out is not None:
-        _, _, _, ob, os_ = _pixels(out, "out", x.shape, x.dtype)
+        _channels_last(out, "out", x.dtype)
+        _shape(out, "out", x.shape)
     dev = _on_one_device(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, bias=bias, out=out,
                          workspace=workspace)
     need = group_norm_workspace_size(B, S, C, groups, x.dtype, True)
     with _launching(dev, stream) as s:
         dx = out
         if dx is None:
-            dx, ob, os_ = torch.empty(x.shape, dtype=x.dtype, device=dev), S * C, C
-        dweight = None if weight is None else torch.empty((C,), dtype=torch.float32, device=dev)
-        dbias = None if bias is None else torch.empty((C,), dtype=torch.float32, device=dev)
+            dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+        _, _, _, ob, os_ = _pixels(dx.shape, dx.stride(), "out")
+        dweight = None if weight is None else torch.empty(C, dtype=torch.float32, device=dev)
+        dbias = None if bias is None else torch.empty(C, dtype=torch.float32, device=dev)
         ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
-        _check(w8a8_group_norm_backward(_ptr(dy), gb, gs, _ptr(x), xb, xs, _DTYPES[x.dtype], B, S, C,
-                                        groups, _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias),
-                                        pdt, act, _ptr(dx), ob, os_, _ptr(dweight), _ptr(dbias),
-                                        ws_ptr, ws_bytes, _stream(s)), "w8a8_group_norm_backward")
+        _check(w8a8_group_norm_backward(dy.data_ptr(), gb, gs, x.data_ptr(), xb, xs,
+                                        _DTYPES[x.dtype], B, S, C, groups, mean.data_ptr(),
+                                        rstd.data_ptr(), _address(weight), _address(bias), pdt, act,
+                                        dx.data_ptr(), ob, os_, _address(dweight), _address(dbias),
+                                        ws_ptr, ws_bytes, _handle(s)), "w8a8_group_norm_backward")
         del ws
     return dx, dweight, dbias
 

@@ -1099,12 +1099,13 @@ int launch_input_grad_swap(const w8a8_plan &plan, const int8_t *codes, const flo
 
 inline int dtype_size(int dtype) { return dtype == W8A8_DTYPE_FP32 ? 4 : 2; }
 
-// Turns per position * 2^64 of a frequency in radians per position.
+// Turns per position * 2^64 (modulo whole turns) of a frequency in radians per
+// position, finite and >= 0.
 unsigned long long turns_q64(double radians) {
-  double t = radians / 6.283185307179586476925286766559;
-  t -= std::floor(t);
-  const double v = std::ldexp(t, 64);
-  return v >= 18446744073709551616.0 ? 0ull : static_cast<unsigned long long>(v);
+  constexpr double kWhole = 18446744073709551616.0;  // 2^64
+  double v = radians * (kWhole / 6.283185307179586476925286766559);
+  if (v >= kWhole) v = std::fmod(v, kWhole);
+  return static_cast<unsigned long long>(v);
 }
 
 // Whether rows that start at p and lie `strides` apart allow 16-byte accesses.
@@ -1117,18 +1118,29 @@ int launch_rotary_t(RotParams &p, bool copy_rest, cudaStream_t stream) {
   const int pairs = p.rot / 2;
   p.rot_units = HALF ? pairs / VEC : p.rot / VEC;
   p.units = p.rot_units + (copy_rest ? (p.dim - p.rot) / VEC : 0);
-  p.bx = p.units < kRotThreads ? p.units : kRotThreads;
-  p.by = kRotThreads / p.bx;
-  // enough tokens that every thread has a few units, fewer while the blocks
-  // would not fill the SMs
+  const int threads = p.units <= 256 ? 256 : kRotThreads;
+  p.bx = p.units;
+  p.by = threads / p.bx;
+  // Tokens per block: a divisor of the thread rows, with which the heads fill
+  // the rows of a token best and give a thread its kRotUnroll loads in flight
+  // (40 heads in 32 rows: 1 token leaves 24 rows idle half the time, 4 tokens
+  // give every thread 5 heads), unless the blocks would then not fill the SMs.
   const int64_t total = static_cast<int64_t>(p.batch) * p.tokens;
-  int64_t nt = cdiv(int64_t{kRotThreads} * kRotUnroll, static_cast<int64_t>(p.units) * p.total_heads);
-  if (nt > kRotMaxTokens) nt = kRotMaxTokens;
-  while (nt > 1 && cdiv(total, nt) < 4 * 148) nt /= 2;
+  int64_t nt = 1, best = 0;
+  for (int64_t t = 1; t <= p.by && t <= kRotMaxTokens; ++t) {
+    if (p.by % t != 0 || (t > 1 && cdiv(total, t) < 4 * 148)) continue;
+    const int64_t each = cdiv(p.total_heads, p.by / t);  // heads per thread
+    const int64_t fill = 1000 * p.total_heads / (each * (p.by / t));
+    const int64_t score = fill * (each < kRotUnroll ? each : kRotUnroll);
+    if (score > best) {
+      best = score;
+      nt = t;
+    }
+  }
   p.block_tokens = static_cast<int32_t>(nt);
   const size_t smem = static_cast<size_t>(nt) * pairs * sizeof(float2);
   return launch(rotary_kernel<T, VEC, HALF, WIDE>, dim3(static_cast<unsigned>(cdiv(total, nt))),
-                dim3(kRotThreads), smem, stream, p);
+                dim3(threads), smem, stream, p);
 }
 
 template <typename T>
@@ -1200,7 +1212,7 @@ size_t norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, int dtyp
 }
 
 void norm_params(NormParams *p, const NormCut &c, int64_t B, int64_t S, int64_t C, int64_t G,
-                 const void *weight, const void *bias, int param_dtype, int silu, void *workspace) {
+                 const void *weight, const void *bias, int param_dtype, void *workspace) {
   std::memset(p, 0, sizeof(*p));
   p->B = static_cast<int32_t>(B);
   p->S = static_cast<int32_t>(S);
@@ -1209,14 +1221,21 @@ void norm_params(NormParams *p, const NormCut &c, int64_t B, int64_t S, int64_t 
   p->tpr = c.tpr;
   p->rpi = c.rpi;
   p->run = c.run;
-  p->group_lanes = 32;
-  while (p->group_lanes > 1 && G * p->group_lanes > kNormThreads) p->group_lanes /= 2;
+  p->group_shift = 5;
+  while (p->group_shift > 0 && (G << p->group_shift) > kNormThreads) --p->group_shift;
+  p->group_channels = static_cast<int32_t>(C / G);
+  p->row_entries = p->group_channels / c.run;
+  p->slab_part = static_cast<int32_t>(S / c.slabs);
+  p->slab_extra = static_cast<int32_t>(S % c.slabs);
+  p->chunks = static_cast<int32_t>(cdiv(p->slab_part, c.rows));
+  p->chunks_longer = static_cast<int32_t>(cdiv(p->slab_part + 1, c.rows));
+  p->many = p->slab_part / c.rpi;
+  p->many_longer = (p->slab_part + 1) / c.rpi;
   p->slabs = static_cast<int32_t>(c.slabs);
   p->teams = static_cast<int32_t>(c.teams);
   p->weight = weight;
   p->bias = bias;
   p->param_f32 = param_dtype == W8A8_DTYPE_FP32 ? 1 : 0;
-  p->silu = silu;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   p->entries = reinterpret_cast<uint4 *>(ws);
   p->readers = reinterpret_cast<unsigned long long *>(ws + norm_entry_bytes(c, B, G));
@@ -1226,7 +1245,7 @@ void norm_params(NormParams *p, const NormCut &c, int64_t B, int64_t S, int64_t 
 
 // One launch.  Blocks that share a sample wait for one another, so the grid
 // (at most one block per SM) is launched cooperatively: all of it runs at once.
-template <typename T, int MODE>
+template <typename T, int MODE, bool SILU>
 int launch_norm_mode(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaStream_t stream) {
   const size_t region =
       MODE == kNormBackward
@@ -1240,15 +1259,15 @@ int launch_norm_mode(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaS
   if (slots > kNormMaxSlots) slots = kNormMaxSlots;
   if (slots > chunks) slots = chunks;
   p.slots = static_cast<int32_t>(slots);
-  constexpr auto kernel = norm_kernel<T, MODE>;
+  constexpr auto kernel = norm_kernel<T, MODE, SILU>;
   int st = ensure_smem_limit<kernel>(d.max_smem_optin - 1024);
   if (st != W8A8_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeCooperative;
   attr.val.cooperative = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(c.teams * c.slabs));
-  cfg.blockDim = dim3(kNormThreads + 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(c.slabs), static_cast<unsigned>(c.teams));
+  cfg.blockDim = dim3(kNormThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(slots * slot) + region;
   cfg.stream = stream;
   cfg.attrs = &attr;
@@ -1261,13 +1280,15 @@ int launch_norm_mode(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaS
 }
 
 template <typename T, bool QUANT>
-int launch_norm(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaStream_t stream) {
-  return launch_norm_mode<T, QUANT ? kNormQuant : kNormForward>(p, c, d, stream);
+int launch_norm(NormParams &p, const NormCut &c, bool silu, const DeviceInfo &d, cudaStream_t stream) {
+  constexpr int M = QUANT ? kNormQuant : kNormForward;
+  return silu ? launch_norm_mode<T, M, true>(p, c, d, stream) : launch_norm_mode<T, M, false>(p, c, d, stream);
 }
 
 template <typename T>
-int launch_norm_grad(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaStream_t stream) {
-  int st = launch_norm_mode<T, kNormBackward>(p, c, d, stream);
+int launch_norm_grad(NormParams &p, const NormCut &c, bool silu, const DeviceInfo &d, cudaStream_t stream) {
+  int st = silu ? launch_norm_mode<T, kNormBackward, true>(p, c, d, stream)
+                : launch_norm_mode<T, kNormBackward, false>(p, c, d, stream);
   if (st != W8A8_OK || (p.dweight == nullptr && p.dbias == nullptr)) return st;
   return launch(norm_grad_params_kernel, dim3(static_cast<unsigned>(cdiv(p.C, 8))), dim3(256), 0,
                 stream, p);
@@ -2026,7 +2047,8 @@ int w8a8_group_norm(const void *x, int64_t x_batch, int64_t x_pixel, int dtype, 
   if (st != W8A8_OK) return st;
   const NormCut c = norm_cut(B, S, C, G, dtype, kNormForward, d->sms);
   NormParams p;
-  norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, activation == W8A8_ACT_SILU, workspace);
+  norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, workspace);
+  const bool silu = activation == W8A8_ACT_SILU;
   p.x = x;
   p.xb = x_batch;
   p.xs = x_pixel;
@@ -2037,9 +2059,9 @@ int w8a8_group_norm(const void *x, int64_t x_batch, int64_t x_pixel, int dtype, 
   p.mean_out = mean_out;
   p.rstd_out = rstd_out;
   switch (dtype) {
-    case W8A8_DTYPE_BF16: return launch_norm<__nv_bfloat16, false>(p, c, *d, stream);
-    case W8A8_DTYPE_FP16: return launch_norm<__half, false>(p, c, *d, stream);
-    default: return launch_norm<float, false>(p, c, *d, stream);
+    case W8A8_DTYPE_BF16: return launch_norm<__nv_bfloat16, false>(p, c, silu, *d, stream);
+    case W8A8_DTYPE_FP16: return launch_norm<__half, false>(p, c, silu, *d, stream);
+    default: return launch_norm<float, false>(p, c, silu, *d, stream);
   }
 }
 
@@ -2064,7 +2086,8 @@ int w8a8_group_norm_quant(const void *x_bf16, int64_t x_batch, int64_t x_pixel, 
   if (st != W8A8_OK) return st;
   const NormCut c = norm_cut(B, S, C, G, W8A8_DTYPE_BF16, kNormQuant, d->sms);
   NormParams p;
-  norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, activation == W8A8_ACT_SILU, workspace);
+  norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, workspace);
+  const bool silu = activation == W8A8_ACT_SILU;
   p.x = x_bf16;
   p.xb = x_batch;
   p.xs = x_pixel;
@@ -2073,7 +2096,7 @@ int w8a8_group_norm_quant(const void *x_bf16, int64_t x_batch, int64_t x_pixel, 
   p.s_q = s_a;
   p.mean_out = mean_out;
   p.rstd_out = rstd_out;
-  return launch_norm<__nv_bfloat16, true>(p, c, *d, stream);
+  return launch_norm<__nv_bfloat16, true>(p, c, silu, *d, stream);
 }
 
 int w8a8_group_norm_backward(const void *dy, int64_t dy_batch, int64_t dy_pixel, const void *x,
@@ -2101,7 +2124,8 @@ int w8a8_group_norm_backward(const void *dy, int64_t dy_batch, int64_t dy_pixel,
   if (st != W8A8_OK) return st;
   const NormCut c = norm_cut(B, S, C, G, dtype, kNormBackward, d->sms);
   NormParams p;
-  norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, activation == W8A8_ACT_SILU, workspace);
+  norm_params(&p, c, B, S, C, G, weight, bias, param_dtype, workspace);
+  const bool silu = activation == W8A8_ACT_SILU;
   p.dy = dy;
   p.dyb = dy_batch;
   p.dys = dy_pixel;
@@ -2116,9 +2140,9 @@ int w8a8_group_norm_backward(const void *dy, int64_t dy_batch, int64_t dy_pixel,
   p.dweight = dweight;
   p.dbias = dbias;
   switch (dtype) {
-    case W8A8_DTYPE_BF16: return launch_norm_grad<__nv_bfloat16>(p, c, *d, stream);
-    case W8A8_DTYPE_FP16: return launch_norm_grad<__half>(p, c, *d, stream);
-    default: return launch_norm_grad<float>(p, c, *d, stream);
+    case W8A8_DTYPE_BF16: return launch_norm_grad<__nv_bfloat16>(p, c, silu, *d, stream);
+    case W8A8_DTYPE_FP16: return launch_norm_grad<__half>(p, c, silu, *d, stream);
+    default: return launch_norm_grad<float>(p, c, silu, *d, stream);
   }
 }
 

@@ -13,9 +13,9 @@
 // Every form needs a sum over a whole sample before it can write its first
 // value, and is bound by memory: one read of the inputs, one write.  One
 // launch does both passes.  A sample's pixels are cut into slabs, one per
-// block, one block per SM, all resident at once (a cooperative launch).  A
-// producer warp streams the slab through a ring of shared memory with bulk
-// copies; the 16 other warps reduce each chunk as it lands.  The last chunks
+// block, one block per SM, all resident at once (a cooperative launch).  The
+// first warp streams the slab through a ring of shared memory with bulk
+// copies; all warps reduce each chunk as it lands.  The last chunks
 // of the first pass stay in the ring, so a slab of up to 192 KB (28 MB over
 // the GPU) is read once; of longer ones the second pass, which runs backwards,
 // reads the rest again, the most recently read chunks first.
@@ -48,11 +48,10 @@
 
 namespace w8a8 {
 
-constexpr int kNormThreads = 512;  // consumers: rpi rows of tpr threads, the rest idle
+constexpr int kNormThreads = 512;  // rpi rows of tpr threads, the rest idle
 constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kNormMaxVecs = 512;  // 16-byte vectors of a pixel: 4096 channels, 2048 in fp32
 constexpr int kNormMaxSlots = 8;
-constexpr int kNormBar = 1;        // named barrier of the consumers
 
 // What a launch computes.
 constexpr int kNormForward = 0, kNormQuant = 1, kNormBackward = 2;
@@ -66,15 +65,19 @@ struct NormParams {
   int64_t xb, xs, dyb, dys, yb, ys;  // strides of a sample and a pixel, elements
   int32_t B, S, C, G;
   int32_t tpr, rpi;                  // threads per row, rows per block iteration
+  int32_t group_channels;            // C / G
+  int32_t slab_part, slab_extra;     // S over slabs: quotient and remainder
+  int32_t chunks, chunks_longer;     // of a slab of slab_part pixels, and of one more
+  int32_t many, many_longer;         // its pixels over rpi
+  int32_t row_entries;               // (C / G) / run
   int32_t run;                       // channels of a vector that surely share a group
-  int32_t group_lanes;               // threads joining a group: 32, fewer where groups are many
+  int32_t group_shift;               // 2^group_shift threads join a group: 32, fewer where groups are many
   int32_t slabs;                     // blocks sharing a sample
-  int32_t teams;                     // samples in flight: gridDim.x / slabs
+  int32_t teams;                     // samples in flight: gridDim.y
   int32_t slots, chunk_bytes;        // of one tensor
   const void *weight, *bias;         // [C] in x's type or fp32, 16-byte aligned, or nullptr
   int32_t param_f32;
   float eps;
-  int32_t silu;
   uint4 *entries;                    // [B][G][slabs] (slabs > 1)
   unsigned long long *readers;       // [B][slabs] (slabs > 1)
   unsigned long long tag;
@@ -85,13 +88,6 @@ struct NormParams {
   float *s_q;
   float *dweight, *dbias;            // [C] or nullptr
 };
-
-// Pixels [lo, hi) of slab j: an even share, the first slabs one more.
-__device__ __forceinline__ void slab_range(int S, int slabs, int j, int &lo, int &hi) {
-  const int per = S / slabs, extra = S % slabs;
-  lo = j * per + (j < extra ? j : extra);
-  hi = lo + per + (j < extra ? 1 : 0);
-}
 
 template <typename T>
 constexpr int kNormVec = 16 / static_cast<int>(sizeof(T));
@@ -168,10 +164,10 @@ __device__ __forceinline__ void norm_param(const void *p, int f32, int ch, float
   }
 }
 
-// f(i, group of channel ch + i) for the V channels from ch on, c a group.
+// f(i, its group) for V adjacent channels, the first of them channel `in` of
+// group g, c a group.
 template <int V, typename F>
-__device__ __forceinline__ void each_group(int ch, int c, F f) {
-  int g = ch / c, in = ch - g * c;
+__device__ __forceinline__ void each_group(int g, int in, int c, F f) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     f(i, g);
@@ -246,12 +242,8 @@ __device__ __forceinline__ bool entry_wait(const uint4 *p, unsigned long long ta
   }
 }
 
-__device__ __forceinline__ bool abort_seen(const int *flag) {
-  return *const_cast<const volatile int *>(flag) != 0;
-}
-
-// The producer warp's loads of one chunk: `rows` rows of `row_bytes` bytes,
-// `step` bytes apart, into dst (adjacent rows in one copy).
+// One warp's loads of a chunk: `rows` rows of `row_bytes` bytes, `step` bytes
+// apart, into dst (adjacent rows in one copy).
 __device__ __forceinline__ void norm_load_rows(uint8_t *dst, const uint8_t *src, int rows,
                                                uint32_t row_bytes, int64_t step, uint64_t *bar,
                                                int lane) {
@@ -263,8 +255,8 @@ __device__ __forceinline__ void norm_load_rows(uint8_t *dst, const uint8_t *src,
   }
 }
 
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid_constant__ NormParams p) {
+template <typename T, int MODE, bool SILU>
+__global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int V = kNormVec<T>, H = V / 2;  // values and pairs of a vector
   constexpr int K = kNormRows<MODE>;
   constexpr bool BWD = MODE == kNormBackward;
@@ -275,89 +267,87 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
   const int slot_bytes = p.chunk_bytes * (BWD ? 2 : 1);
   // [slots][x rows, dy rows] | the statistics' region | row maxima (int8 form)
   float2 *region = reinterpret_cast<float2 *>(norm_smem + NS * slot_bytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunk_rows = p.rpi * K;
   const uint32_t row_bytes = static_cast<uint32_t>(p.C) * sizeof(T);
-  const int team = blockIdx.x / p.slabs, slab = blockIdx.x - team * p.slabs;
-  int lo, hi;
-  slab_range(p.S, p.slabs, slab, lo, hi);
-  const int chunks = (hi - lo + chunk_rows - 1) / chunk_rows;
+  // pixels [lo, lo + pixels) of the samples team, team + teams, ...: the first
+  // slabs one more
+  const int slab = blockIdx.x;
+  const bool longer = slab < p.slab_extra;
+  const int lo = slab * p.slab_part + (longer ? slab : p.slab_extra);
+  const int pixels = p.slab_part + (longer ? 1 : 0);
+  const int chunks = longer ? p.chunks_longer : p.chunks;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kNormWarps);
-    }
-    abort_flag = 0;
-    fence_mbarrier_init();
-  }
-  __syncthreads();
-
-  if (warp == kNormWarps) {
-    // ------------------------------------------------------------ producer
-    uint32_t used = 0, empty_par = 0, full_par = 0;  // bit s: slot s
-    bool ok = true;
-    auto fill = [&](int b, int chunk) {
-      const int s = chunk % NS;
-      const uint32_t bit = 1u << s;
-      if (used & bit) {
-        ok = mbar_wait(&empty[s], (empty_par & bit) ? 1u : 0u, &abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) return;
-        empty_par ^= bit;
-        full_par ^= bit;
-      }
-      used |= bit;
-      const int r0 = lo + chunk * chunk_rows;
-      const int rows = hi - r0 < chunk_rows ? hi - r0 : chunk_rows;
-      if (lane == 0) mbar_arrive_expect_tx(&full[s], rows * row_bytes * (BWD ? 2u : 1u));
-      __syncwarp();
-      uint8_t *dst = norm_smem + s * slot_bytes;
-      norm_load_rows(dst, static_cast<const uint8_t *>(p.x) + (b * p.xb + r0 * p.xs) * static_cast<int64_t>(sizeof(T)),
-                     rows, row_bytes, p.xs * static_cast<int64_t>(sizeof(T)), &full[s], lane);
-      if constexpr (BWD)
-        norm_load_rows(dst + p.chunk_bytes,
-                       static_cast<const uint8_t *>(p.dy) + (b * p.dyb + r0 * p.dys) * static_cast<int64_t>(sizeof(T)),
-                       rows, row_bytes, p.dys * static_cast<int64_t>(sizeof(T)), &full[s], lane);
-    };
-    for (int b = team; ok && b < p.B; b += p.teams) {
-      for (int i = 0; ok && i < chunks; ++i) fill(b, i);
-      for (int i = chunks - NS - 1; ok && i >= 0; --i) fill(b, i);
-      if (p.slabs > 1 && slab == 0 && ok) {
-        // once every block has read the sample's entries: their tags go
-        for (int j = lane; j < p.slabs; j += 32) {
-          unsigned long long *r = p.readers + static_cast<int64_t>(b) * p.slabs + j;
-          const uint64_t t0 = global_timer_ns();
-          for (uint32_t i = 1; ok && ld_acquire_gpu_u64(r) != p.tag; ++i) {
-            if ((i & 15u) == 0u && (abort_seen(&abort_flag) || global_timer_ns() - t0 > kWaitLimitNs)) {
-              if (!abort_seen(&abort_flag)) atomicOr(&g_device_error, W8A8_DEVERR_TIMEOUT);
-              ok = false;
-            }
-          }
-          if (ok) *reinterpret_cast<volatile unsigned long long *>(r) = 0ull;
-        }
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        uint4 *e = p.entries + static_cast<int64_t>(b) * p.G * p.slabs;
-        for (int i = lane; ok && i < p.G * p.slabs; i += 32) entry_store(e + i, make_float2(0.0f, 0.0f), 0ull);
-      }
-    }
-    // copies still in flight (after an abort) land before the block leaves
-    for (int s = 0; s < NS; ++s) {
-      volatile int never = 0;
-      if (used & (1u << s)) mbar_wait(&full[s], (full_par >> s) & 1u, &never);
-    }
-    return;
-  }
-
-  // -------------------------------------------------------------- consumers
-  const int tid = threadIdx.x;
-  const int row = tid / p.tpr, vec = tid - row * p.tpr;
-  const bool live = row < p.rpi;
-  const int c = p.C / p.G;
-  const uint32_t offset = static_cast<uint32_t>(row) * row_bytes + vec * 16u;
-  const uint32_t row_step = static_cast<uint32_t>(p.rpi) * row_bytes;
+  // ---- loads, issued by the first warp.  A slot is filled again once all
+  // warps have released it; the refill is asked for a chunk later, when the
+  // others have caught up.
+  uint32_t used = 0, empty_par = 0, fill_par = 0;  // bit s: slot s (first warp)
   uint32_t full_par = 0;
   bool ok = true;  // after a wait gave up the flow goes on, but stores nothing
+  auto fill = [&](int b, int chunk, int s) {
+    const uint32_t bit = 1u << s;
+    if (used & bit) {
+      if (ok) ok = mbar_wait(&empty[s], (empty_par & bit) ? 1u : 0u, &abort_flag);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) return;
+      empty_par ^= bit;
+      fill_par ^= bit;
+    }
+    used |= bit;
+    const int r0 = lo + chunk * chunk_rows;
+    const int rows = lo + pixels - r0 < chunk_rows ? lo + pixels - r0 : chunk_rows;
+    if (lane == 0) mbar_arrive_expect_tx(&full[s], rows * row_bytes * (BWD ? 2u : 1u));
+    __syncwarp();
+    uint8_t *dst = norm_smem + s * slot_bytes;
+    norm_load_rows(dst, static_cast<const uint8_t *>(p.x) + (b * p.xb + r0 * p.xs) * static_cast<int64_t>(sizeof(T)),
+                   rows, row_bytes, p.xs * static_cast<int64_t>(sizeof(T)), &full[s], lane);
+    if constexpr (BWD)
+      norm_load_rows(dst + p.chunk_bytes,
+                     static_cast<const uint8_t *>(p.dy) + (b * p.dyb + r0 * p.dys) * static_cast<int64_t>(sizeof(T)),
+                     rows, row_bytes, p.dys * static_cast<int64_t>(sizeof(T)), &full[s], lane);
+  };
+  const int row = tid / p.tpr, vec = tid - row * p.tpr;
+  const bool live = row < p.rpi;
+  const int c = p.group_channels;
+  const int group0 = vec * V / c, in0 = vec * V - group0 * c;  // the vector's first channel
+  // Gradient: per channel rstd, -mean, weight and bias.  Loaded before the
+  // first copies are asked for: a whole ring per block (28 MB over the GPU)
+  // would be ahead of these few values (measured: 5.5 us of wait, 3.0 before).
+  float2 rs[H], nm[H], wt[H], bs[H];
+  auto load_params = [&](int b) {
+    if (BWD && live) {
+      norm_param<T>(p.weight, p.param_f32, vec * V, 1.0f, wt);
+      norm_param<T>(p.bias, p.param_f32, vec * V, 0.0f, bs);
+      const int64_t at0 = static_cast<int64_t>(b) * p.G;
+      each_group<V>(group0, in0, c, [&](int i, int g) {
+        at(nm, i) = -__ldg(p.mean_in + at0 + g);
+        at(rs, i) = __ldg(p.rstd_in + at0 + g);
+      });
+    }
+  };
+  load_params(blockIdx.y);
+  if constexpr (BWD) __syncthreads();
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int s = 0; s < NS; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], kNormWarps);
+      }
+      abort_flag = 0;
+      fence_mbarrier_init();
+    }
+    __syncwarp();
+    for (int i = 0; i < NS && i < chunks; ++i) fill(blockIdx.y, i, i);
+  }
+  const uint32_t offset = static_cast<uint32_t>(row) * row_bytes + vec * 16u;
+  const uint32_t row_step = static_cast<uint32_t>(p.rpi) * row_bytes;
+  // this thread's rows of the last chunk
+  int last_nb = 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    last_nb += live && (chunks - 1) * chunk_rows + row + k * p.rpi < pixels ? 1 : 0;
+  __syncthreads();
+
   auto arrive_full = [&](int s) {
     if (ok) ok = mbar_wait(&full[s], (full_par >> s) & 1u, &abort_flag);
     full_par ^= 1u << s;
@@ -367,19 +357,11 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
     if (lane == 0) mbar_arrive(&empty[s]);
   };
 
-  for (int b = team; b < p.B; b += p.teams) {
-    // gradient: per channel rstd, -mean, weight and bias
-    float2 rs[H], nm[H], wt[H], bs[H];
-    if constexpr (BWD) {
-      if (live) {
-        norm_param<T>(p.weight, p.param_f32, vec * V, 1.0f, wt);
-        norm_param<T>(p.bias, p.param_f32, vec * V, 0.0f, bs);
-        const int64_t at0 = static_cast<int64_t>(b) * p.G;
-        each_group<V>(vec * V, c, [&](int i, int g) {
-          at(nm, i) = -__ldg(p.mean_in + at0 + g);
-          at(rs, i) = __ldg(p.rstd_in + at0 + g);
-        });
-      }
+  for (int b = blockIdx.y; b < p.B; b += p.teams) {
+    if (b != static_cast<int>(blockIdx.y)) {
+      load_params(b);
+      if (warp == 0)
+        for (int i = 0; i < NS && i < chunks; ++i) fill(b, i, i);
     }
     // xh and dz of a vector (gradient)
     auto grad_vec = [&](uint4 xv, uint4 gv, float2 (&xh)[H], float2 (&dz)[H]) {
@@ -388,7 +370,7 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         xh[i] = mul2_rn(add2_rn(xh[i], nm[i]), rs[i]);
-        if (p.silu) {  // y'(z) = s + z s (1 - s)
+        if constexpr (SILU) {  // y'(z) = s + z s (1 - s)
           const float2 z = fma2_rn(xh[i], wt[i], bs[i]);
           const float2 s = sigmoid2(z);
           const float2 zs = mul2_rn(z, s);
@@ -472,12 +454,10 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
       arrive_full(slot);
       if (live) reduce(norm_smem + slot * slot_bytes + offset, K, std::true_type{});
       if (i + NS < chunks) release(slot);  // the last chunks stay for the second pass
+      const int before = slot == 0 ? NS - 1 : slot - 1;
+      if (warp == 0 && i > 0 && i - 1 + NS < chunks) fill(b, i - 1 + NS, before);
       slot = slot + 1 == NS ? 0 : slot + 1;
     }
-    // this thread's rows of the last chunk
-    const int last_left = hi - lo - (chunks - 1) * chunk_rows - row;
-    const int last_have = live && last_left > 0 ? (last_left + p.rpi - 1) / p.rpi : 0;
-    const int last_nb = last_have < K ? last_have : K;
     arrive_full(slot);
     if (last_nb == K)
       reduce(norm_smem + slot * slot_bytes + offset, K, std::true_type{});
@@ -486,11 +466,10 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
 
     // ---- the slab's groups.  A thread first joins runs of `run` channels of
     // its vector that share a group; region[row][vec * (V / run) + i].
-    const int run = p.run, per = V / run;   // 1, 2, 4 or 8 channels
-    const int width = p.tpr * per;          // entries of a row
-    const int cpg = c / run;                // entries of a group in a row
-    const int pixels = hi - lo;
-    named_barrier_sync(kNormBar, kNormThreads);  // the region is free again
+    const int run = p.run;                  // 1, 2, 4 or 8 channels
+    const int width = p.row_entries * p.G;  // entries of a row
+    const int cpg = p.row_entries;          // entries of a group in a row
+    __syncthreads();  // the region is free again
     if (live) {
       float a[V], d[V];
 #pragma unroll
@@ -529,11 +508,12 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
         }
       }
     }
-    named_barrier_sync(kNormBar, kNormThreads);
+    __syncthreads();
     if constexpr (BWD) {
       // per channel over the rows, to global memory; weighted in place
       for (int ch = tid; ch < p.C; ch += kNormThreads) {
         float2 t = region[ch];
+#pragma unroll 8
         for (int r = 1; r < p.rpi; ++r) {
           t.x += region[r * p.C + ch].x;
           t.y += region[r * p.C + ch].y;
@@ -545,14 +525,14 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
                           : to_f32<T>(static_cast<const T *>(p.weight)[ch]);
         region[ch] = make_float2(w * t.x, w * t.y);
       }
-      named_barrier_sync(kNormBar, kNormThreads);
+      __syncthreads();
     }
     // `lanes` neighbouring threads per group join its entries, publish them
     // or (alone) finish the group.  All groups at once up to 512 of them.
     float2 *stat = region + (BWD ? p.C : p.rpi * width);
     const float count = static_cast<float>(p.S) * c;  // values of a group
     uint4 *const entries = p.entries + static_cast<int64_t>(b) * p.G * p.slabs;
-    const int lanes = p.group_lanes, sub = tid & (lanes - 1);
+    const int lanes = 1 << p.group_shift, sub = tid & (lanes - 1);
     auto group_sum = [&](float v) {
       for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
       return v;
@@ -560,9 +540,9 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
     auto finish = [&](float2 t) {
       return BWD ? make_float2(t.x / count, t.y / count) : make_float2(t.x, rsqrtf(t.y / count + p.eps));
     };
-    const int gstep = kNormThreads / lanes;
+    const int gstep = kNormThreads >> p.group_shift;
     for (int g0 = 0; g0 < p.G; g0 += gstep) {  // whole warps stay together
-      const int g = g0 + tid / lanes;
+      const int g = g0 + (tid >> p.group_shift);
       float2 mine = make_float2(0.0f, 0.0f);
       if constexpr (BWD) {
         if (g < p.G) {
@@ -575,11 +555,12 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
       } else {
         // entry e: `run` channels of the group in row e / cpg, standing for
         // the row's pixels.  Rows below pixels % rpi have one pixel more.
-        const int many = pixels / p.rpi, more = pixels - many * p.rpi;
+        const int many = longer ? p.many_longer : p.many, more = pixels - many * p.rpi;
         const int total = p.rpi * cpg;
         const float2 *from = region + g * cpg;
         if (g < p.G) {
-          int r = sub / cpg, col = sub - r * cpg;
+          int r = 0, col = sub;
+          for (; col >= cpg; col -= cpg) ++r;
           for (int e = sub; e < total; e += lanes) {
             mine.x += static_cast<float>(many + (r < more ? 1 : 0)) * from[r * width + col].x;
             for (col += lanes; col >= cpg; col -= cpg) ++r;
@@ -587,7 +568,8 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
         }
         const float mean = group_sum(mine.x) / (static_cast<float>(pixels) * cpg);
         if (g < p.G) {
-          int r = sub / cpg, col = sub - r * cpg;
+          int r = 0, col = sub;
+          for (; col >= cpg; col -= cpg) ++r;
           for (int e = sub; e < total; e += lanes) {
             const float2 st = from[r * width + col];
             const float dd = st.x - mean;
@@ -613,9 +595,9 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
     // ---- the sample's groups, from every block's entry
     if (p.slabs > 1) {
       constexpr int E = 10;  // entries a lane keeps in registers
-      const int part = p.S / p.slabs, extra = p.S - part * p.slabs;
+      const int part = p.slab_part, extra = p.slab_extra;
       for (int g0 = 0; g0 < p.G; g0 += gstep) {
-        const int g = g0 + tid / lanes;
+        const int g = g0 + (tid >> p.group_shift);
         const uint4 *e = entries + static_cast<int64_t>(g) * p.slabs;
         float2 v[E], t = make_float2(0.0f, 0.0f);
         if (p.slabs <= E * lanes) {
@@ -675,7 +657,7 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
     }
-    named_barrier_sync(kNormBar, kNormThreads);
+    __syncthreads();
     if (p.slabs > 1 && tid == 0 && ok) {  // this block has read the sample's entries
       __threadfence();
       *reinterpret_cast<volatile unsigned long long *>(p.readers + static_cast<int64_t>(b) * p.slabs + slab) = p.tag;
@@ -691,7 +673,7 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
     // forward: y = act((x + k3) * k1 + k2); gradient: dx = dz * k1 + k2 + xh * k3
     float2 k1[H], k2[H], k3[H];
     if (live) {
-      each_group<V>(vec * V, c, [&](int i, int g) {
+      each_group<V>(group0, in0, c, [&](int i, int g) {
         const float2 st = stat[g];
         if constexpr (BWD) {
           const float r = at(rs, i);
@@ -708,115 +690,175 @@ __global__ void __launch_bounds__(kNormThreads + 32, 1) norm_kernel(const __grid
     uint32_t *row_max = reinterpret_cast<uint32_t *>(stat + p.G);  // int8 form: [3][chunk_rows]
     if constexpr (MODE == kNormQuant) {
       for (int i = tid; i < 3 * chunk_rows; i += kNormThreads) row_max[i] = 0u;
-      named_barrier_sync(kNormBar, kNormThreads);
+      __syncthreads();
     }
     int turn = 0;
     const bool one_row = (p.tpr & 31) == 0;        // a warp's threads share a row
     const int first = __shfl_sync(0xFFFFFFFFu, row, 0);
-    for (int i = chunks - 1; i >= 0; --i) {
-      const int r0 = lo + i * chunk_rows;
-      const int nb = i == chunks - 1 ? last_nb : (live ? K : 0);
-      if (i < chunks - NS) arrive_full(slot);
-      const uint8_t *src = norm_smem + slot * slot_bytes + offset;
-      if constexpr (MODE == kNormQuant) {
-        static_assert(V == 8 || MODE != kNormQuant, "int8 rows are made of bf16 activations");
-        uint32_t *mx = row_max + turn * chunk_rows;
-        float2 z[K][H];
+    // where this thread's first row of a chunk goes, from the last chunk down
+    uint8_t *dst = nullptr;
+    int64_t dst_row = 0, dst_chunk = 0;
+    int64_t pix = static_cast<int64_t>(b) * p.S + lo + static_cast<int64_t>(chunks - 1) * chunk_rows + row;
+    if constexpr (MODE != kNormQuant) {
+      dst = static_cast<uint8_t *>(p.y) +
+            (b * p.yb + (lo + static_cast<int64_t>(chunks - 1) * chunk_rows + row) * p.ys + vec * V) *
+                static_cast<int64_t>(sizeof(T));
+      dst_row = p.rpi * p.ys * static_cast<int64_t>(sizeof(T));
+      dst_chunk = dst_row * K;
+    }
+    // K rows (`all`), or nb of them: no branch between rows where there are K,
+    // so that their work interleaves
+    auto apply = [&](const uint8_t *src, int nb, auto all) {
+      constexpr bool ALL = decltype(all)::value;
+      // the int8 form's rows meet at a barrier, so its idle threads come too
+      const bool here = MODE != kNormQuant || live;
+      float2 z[K][H];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          float m = 0.0f;
-          if (k < nb) {
-            Pairs<T>::get(*reinterpret_cast<const uint4 *>(src + k * row_step), z[k]);
+      for (int k = 0; k < K; ++k) {
+        if (here && (ALL || k < nb)) {
+          const uint4 xv = *reinterpret_cast<const uint4 *>(src + k * row_step);
+          if constexpr (BWD) {
+            float2 xh[H];
+            grad_vec(xv, *reinterpret_cast<const uint4 *>(src + p.chunk_bytes + k * row_step), xh, z[k]);
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+              z[k][h] = fma2_rn(z[k][h], k1[h], fma2_rn(xh[h], k3[h], k2[h]));
+          } else {
+            Pairs<T>::get(xv, z[k]);
 #pragma unroll
             for (int h = 0; h < H; ++h) {
               z[k][h] = fma2_rn(add2_rn(z[k][h], k3[h]), k1[h], k2[h]);
-              if (p.silu) z[k][h] = mul2_rn(z[k][h], sigmoid2(z[k][h]));
-              m = fmaxf(m, fmaxf(fabsf(z[k][h].x), fabsf(z[k][h].y)));
+              if constexpr (SILU) z[k][h] = mul2_rn(z[k][h], sigmoid2(z[k][h]));
             }
-          }
-          // A row's threads are neighbours: a warp holds one or two rows, or,
-          // of narrow rows, several.  One maximum per warp and row goes to
-          // shared memory (maxima do not depend on the order).
-          const uint32_t mb = __float_as_uint(m);
-          if (one_row) {
-            const uint32_t m0 = __reduce_max_sync(0xFFFFFFFFu, mb);
-            if (lane == 0 && k < nb) atomicMax(mx + row + k * p.rpi, m0);
-          } else if (p.tpr > 32) {
-            const uint32_t m0 = __reduce_max_sync(0xFFFFFFFFu, row == first ? mb : 0u);
-            const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, row == first ? 0u : mb);
-            if (lane == 0) {
-              if (first < p.rpi) atomicMax(mx + first + k * p.rpi, m0);
-              if (first + 1 < p.rpi) atomicMax(mx + first + 1 + k * p.rpi, m1);
-            }
-          } else if (k < nb) {
-            atomicMax(mx + row + k * p.rpi, mb);
-          }
-        }
-        named_barrier_sync(kNormBar, kNormThreads);
-        // the maxima of two chunks ago are no longer read: clear them for the
-        // chunk after the next
-        uint32_t *old = row_max + (turn == 0 ? 2 : turn - 1) * chunk_rows;
-        for (int r = tid; r < chunk_rows; r += kNormThreads) old[r] = 0u;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          if (k < nb && ok) {
-            const float amax = __uint_as_float(mx[row + k * p.rpi]);
-            // rint(y * (127 / amax)) in one fused step: y is a rounded fp32
-            // value already, so a quotient off by 2^-22 moves a code only
-            // where y is that close to a tie; the scale is the IEEE quotient.
-            // Next to the subnormals, where 127 / amax leaves fp32, divide.
-            uint32_t code[V];
-            if (amax >= 1e-30f) {
-              const float r = __fdividef(127.0f, amax);
-#pragma unroll
-              for (int h = 0; h < H; ++h) {
-                const float2 t = fma2_rn(z[k][h], make_float2(r, r), make_float2(kRintMagic, kRintMagic));
-                code[2 * h] = __float_as_uint(t.x);
-                code[2 * h + 1] = __float_as_uint(t.y);
-              }
-            } else {
-              const float sc = __fdiv_rn(amax, 127.0f);
-#pragma unroll
-              for (int h = 0; h < H; ++h) {
-                code[2 * h] = sc == 0.0f ? 0u : quant_exact(z[k][h].x, sc);
-                code[2 * h + 1] = sc == 0.0f ? 0u : quant_exact(z[k][h].y, sc);
-              }
-            }
-            const int64_t pix = static_cast<int64_t>(b) * p.S + r0 + row + k * p.rpi;
-            *reinterpret_cast<uint2 *>(p.q + pix * p.C + vec * V) = pack_codes(code);
-            if (vec == 0) p.s_q[pix] = __fdiv_rn(amax, 127.0f);
-          }
-        }
-        turn = turn == 2 ? 0 : turn + 1;
-      } else {
-        uint8_t *dst = static_cast<uint8_t *>(p.y) +
-                       (b * p.yb + (r0 + row) * p.ys + vec * V) * static_cast<int64_t>(sizeof(T));
-        const int64_t dst_step = p.rpi * p.ys * static_cast<int64_t>(sizeof(T));
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          if (k < nb && ok) {
-            float2 z[H];
-            if constexpr (BWD) {
-              float2 xh[H];
-              grad_vec(*reinterpret_cast<const uint4 *>(src + k * row_step),
-                       *reinterpret_cast<const uint4 *>(src + p.chunk_bytes + k * row_step), xh, z);
-#pragma unroll
-              for (int h = 0; h < H; ++h)
-                z[h] = fma2_rn(z[h], k1[h], fma2_rn(xh[h], k3[h], k2[h]));
-            } else {
-              Pairs<T>::get(*reinterpret_cast<const uint4 *>(src + k * row_step), z);
-#pragma unroll
-              for (int h = 0; h < H; ++h) {
-                z[h] = fma2_rn(add2_rn(z[h], k3[h]), k1[h], k2[h]);
-                if (p.silu) z[h] = mul2_rn(z[h], sigmoid2(z[h]));
-              }
-            }
-            *reinterpret_cast<uint4 *>(dst + k * dst_step) = Pairs<T>::put(z);
           }
         }
       }
+      if constexpr (MODE != kNormQuant) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (ALL || k < nb) *reinterpret_cast<uint4 *>(dst + k * dst_row) = Pairs<T>::put(z[k]);
+        return;
+      }
+      // int8 rows.  A row's threads are neighbours: a warp holds one or two
+      // rows, or, of narrow rows, several.  One maximum per warp and row goes
+      // to shared memory (maxima do not depend on the order).
+      uint32_t *mx = row_max + turn * chunk_rows;
+      uint32_t mb[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float m = 0.0f;
+        if (here && (ALL || k < nb)) {
+#pragma unroll
+          for (int h = 0; h < H; ++h) m = fmaxf(m, fmaxf(fabsf(z[k][h].x), fabsf(z[k][h].y)));
+        }
+        mb[k] = __float_as_uint(m);
+      }
+      if (one_row) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) mb[k] = __reduce_max_sync(0xFFFFFFFFu, mb[k]);
+        if (lane == 0 && live) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) atomicMax(mx + row + k * p.rpi, mb[k]);
+        }
+      } else if (p.tpr > 32) {
+        uint32_t m1[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          m1[k] = __reduce_max_sync(0xFFFFFFFFu, row == first ? 0u : mb[k]);
+          mb[k] = __reduce_max_sync(0xFFFFFFFFu, row == first ? mb[k] : 0u);
+        }
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            if (first < p.rpi) atomicMax(mx + first + k * p.rpi, mb[k]);
+            if (first + 1 < p.rpi) atomicMax(mx + first + 1 + k * p.rpi, m1[k]);
+          }
+        }
+      } else if (live) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) atomicMax(mx + row + k * p.rpi, mb[k]);
+      }
+      __syncthreads();
+      // the maxima of two chunks ago are no longer read: clear them for the
+      // chunk after the next
+      uint32_t *old = row_max + (turn == 0 ? 2 : turn - 1) * chunk_rows;
+      for (int r = tid; r < chunk_rows; r += kNormThreads) old[r] = 0u;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (here && (ALL || k < nb)) {
+          // rint(y * (127 / amax)) in one fused step: y is a rounded fp32
+          // value already, so a quotient off by 2^-22 moves a code only where
+          // y is that close to a tie; the scale is the IEEE quotient.  Next to
+          // the subnormals, where 127 / amax leaves fp32, divide.
+          const float amax = __uint_as_float(mx[row + k * p.rpi]);
+          uint32_t code[V];
+          if (amax >= 1e-30f) {
+            const float r = __fdividef(127.0f, amax);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              const float2 t = fma2_rn(z[k][h], make_float2(r, r), make_float2(kRintMagic, kRintMagic));
+              code[2 * h] = __float_as_uint(t.x);
+              code[2 * h + 1] = __float_as_uint(t.y);
+            }
+          } else {
+            const float sc = __fdiv_rn(amax, 127.0f);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              code[2 * h] = sc == 0.0f ? 0u : quant_exact(z[k][h].x, sc);
+              code[2 * h + 1] = sc == 0.0f ? 0u : quant_exact(z[k][h].y, sc);
+            }
+          }
+          if constexpr (V == 8) {
+            if (ok) {
+              *reinterpret_cast<uint2 *>(p.q + (pix + k * p.rpi) * p.C + vec * V) = pack_codes(code);
+              if (vec == 0) p.s_q[pix + k * p.rpi] = __fdiv_rn(amax, 127.0f);
+            }
+          }
+        }
+      }
+      turn = turn == 2 ? 0 : turn + 1;
+    };
+    for (int i = chunks - 1; i >= 0; --i) {
+      if (i < chunks - NS) arrive_full(slot);
+      if (warp == 0 && i + 1 < chunks && i + 1 >= NS) fill(b, i + 1 - NS, slot + 1 == NS ? 0 : slot + 1);
+      const uint8_t *src = norm_smem + slot * slot_bytes + offset;
+      // the int8 form's rows meet at a barrier: every thread takes part
+      if (i < chunks - 1 ? (live || MODE == kNormQuant) : last_nb == K && MODE != kNormQuant) {
+        if (ok || MODE == kNormQuant) apply(src, K, std::true_type{});
+      } else if (i == chunks - 1 && (last_nb > 0 || MODE == kNormQuant)) {
+        if (ok || MODE == kNormQuant) apply(src, last_nb, std::false_type{});
+      }
       release(slot);
       slot = slot == 0 ? NS - 1 : slot - 1;
+      dst -= dst_chunk;
+      pix -= chunk_rows;
+    }
+    if (p.slabs > 1 && slab == 0 && ok) {
+      // once every block has read the sample's entries: their tags go
+      for (int j = tid; j < p.slabs && ok; j += kNormThreads) {
+        unsigned long long *r = p.readers + static_cast<int64_t>(b) * p.slabs + j;
+        const uint64_t t0 = global_timer_ns();
+        for (uint32_t i = 1; ok && ld_acquire_gpu_u64(r) != p.tag; ++i) {
+          if ((i & 15u) == 0u && global_timer_ns() - t0 > kWaitLimitNs) {
+            abort_flag = 1;
+            atomicOr(&g_device_error, W8A8_DEVERR_TIMEOUT);
+            ok = false;
+          }
+        }
+        if (ok) *reinterpret_cast<volatile unsigned long long *>(r) = 0ull;
+      }
+      if (__syncthreads_and(ok)) {
+        uint4 *e = p.entries + static_cast<int64_t>(b) * p.G * p.slabs;
+        for (int i = tid; i < p.G * p.slabs; i += kNormThreads) entry_store(e + i, make_float2(0.0f, 0.0f), 0ull);
+      } else {
+        ok = false;
+      }
+    }
+  }
+  if (warp == 0 && !ok) {  // copies still in flight land before the block leaves
+    for (int s = 0; s < NS; ++s) {
+      volatile int never = 0;
+      if (used & (1u << s)) mbar_wait(&full[s], (fill_par >> s) & 1u, &never);
     }
   }
 }

@@ -13,10 +13,12 @@
 // |pos| * 2^-65 turns (1.5e-9 at 2^36), and its top 32 bits go to sincospif.
 //
 // Bound by memory: every value is read once and written once.  A block takes
-// a few tokens, computes their cosines and sines once into shared memory (one
-// sincospif per pair and token instead of one per pair, token and head), and
-// walks over the heads with each thread staying on its place within the head,
-// so the factors stay in registers.
+// one or a few tokens.  Each thread keeps one place within the head and one
+// token, asks for its first heads' values, and only then computes its share of
+// the block's cosines and sines (one sincospif per pair and token instead of
+// one per pair, token and head) into shared memory: the loads cover the
+// latency of positions and sines, and the factors stay in registers over the
+// heads.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -30,7 +32,7 @@ namespace w8a8 {
 constexpr int kRotMaxDim = 512;
 constexpr int kRotMaxPairs = kRotMaxDim / 2;
 constexpr int kRotMaxAxes = 8;
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 512;  // at most; 256 where a head's units fit
 constexpr int kRotMaxTokens = 16;  // tokens a block takes at most
 constexpr int kRotUnroll = 4;      // heads in flight per thread
 
@@ -47,10 +49,10 @@ struct RotParams {
   int32_t total_heads;    // of both tensors
   int32_t batch, tokens;  // batch * tokens < 2^31
   int32_t dim, rot;
-  int32_t block_tokens;   // tokens a block takes
+  int32_t block_tokens;   // tokens a block takes: divides by
   int32_t units;          // a head's units of work: rotated ones, then copied ones
   int32_t rot_units;
-  int32_t bx, by;         // threads along the units and along the heads
+  int32_t bx, by;         // threads along the units; along tokens and heads
   const void *pos;
   int32_t pos_is_64, axes;
   int64_t pos_b, pos_t;   // strides of pos in elements; its axes are adjacent
@@ -108,16 +110,48 @@ __global__ void __launch_bounds__(kRotThreads)
   extern __shared__ float2 turn[];  // [block_tokens][rot / 2]: scale * (cos, sin)
   using IO = VecIO<T, VEC, WIDE>;
   constexpr int NP = HALF ? VEC : VEC / 2;  // pairs of a rotated unit
-  const int pairs = p.rot >> 1;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.block_tokens;
-  const int64_t left = static_cast<int64_t>(p.batch) * p.tokens - first;
-  const int nt = left < p.block_tokens ? static_cast<int>(left) : p.block_tokens;
+  constexpr int U = kRotUnroll;
+  const int pairs = p.rot >> 1, nt = p.block_tokens;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * nt;
+  const int64_t total = static_cast<int64_t>(p.batch) * p.tokens;
 
-  for (int i = threadIdx.x; i < nt * pairs; i += kRotThreads) {
-    const int tt = i / pairs, pair = i - tt * pairs;
-    const int at = static_cast<int>(first) + tt;
-    const int b = at / p.tokens, tok = at - b * p.tokens;
-    const int64_t off = b * p.pos_b + tok * p.pos_t + p.axis[pair];
+  // this thread: unit u of the heads h, h + rows, ... of token tt of the block
+  const int ty = threadIdx.x / p.bx, u = threadIdx.x - ty * p.bx;
+  const int rows = p.by / nt;
+  const int h_first = ty / nt, tt = ty - h_first * nt;
+  const bool active = h_first < rows && first + tt < total;
+  const bool rotated = u < p.rot_units;
+  const int v0 = rotated ? u * VEC : p.rot + (u - p.rot_units) * VEC;  // first value in the head
+  const int at = static_cast<int>(first) + tt;
+  const int b = at / p.tokens, tok = at - b * p.tokens;
+  T va[U][VEC], vb[HALF ? U : 1][VEC];
+  // heads h, h + rows, ... (U of them): their place in x or y
+  auto place = [&](int h, bool to) -> int64_t {
+    const RotHeads &t = p.t[h >= p.t[0].heads ? 1 : 0];
+    const int hh = h >= p.t[0].heads ? h - p.t[0].heads : h;
+    return (to ? b * t.yb + tok * t.yt + hh * t.yh : b * t.xb + tok * t.xt + hh * t.xh) + v0;
+  };
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int h = h0 + j * rows;
+      if (h < p.total_heads) {
+        const T *src = static_cast<const T *>(p.t[h >= p.t[0].heads ? 1 : 0].x) + place(h, false);
+        IO::load(src, va[j]);
+        if constexpr (HALF) {
+          if (rotated) IO::load(src + pairs, vb[j]);
+        }
+      }
+    }
+  };
+  if (active) load(h_first);
+
+  const int here = total - first < nt ? static_cast<int>(total - first) : nt;
+  for (int i = threadIdx.x; i < here * pairs; i += blockDim.x) {
+    const int it = i / pairs, pair = i - it * pairs;
+    const int iat = static_cast<int>(first) + it;
+    const int ib = iat / p.tokens, itok = iat - ib * p.tokens;
+    const int64_t off = ib * p.pos_b + itok * p.pos_t + p.axis[pair];
     const long long pos = p.pos_is_64 ? static_cast<const long long *>(p.pos)[off]
                                       : static_cast<const int *>(p.pos)[off];
     const unsigned long long turns = static_cast<unsigned long long>(pos) * p.freq[pair];
@@ -128,68 +162,47 @@ __global__ void __launch_bounds__(kRotThreads)
     turn[i] = make_float2(c * p.scale, (p.backward ? -s : s) * p.scale);
   }
   __syncthreads();
+  if (!active) return;
 
-  const int tx = threadIdx.x % p.bx, ty = threadIdx.x / p.bx;
-  if (ty >= p.by) return;
-  for (int u = tx; u < p.units; u += p.bx) {
-    const bool rotated = u < p.rot_units;
-    // first value of the unit within the head
-    const int v0 = rotated ? u * VEC : p.rot + (u - p.rot_units) * VEC;
-    for (int tt = 0; tt < nt; ++tt) {
-      const int at = static_cast<int>(first) + tt;
-      const int b = at / p.tokens, tok = at - b * p.tokens;
-      float cs[NP], sn[NP];
-      if (rotated) {
-        const float2 *f = turn + tt * pairs + (HALF ? v0 : v0 >> 1);
+  float cs[NP], sn[NP];
+  if (rotated) {
+    const float2 *f = turn + tt * pairs + (HALF ? v0 : v0 >> 1);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const float2 v = f[i];
-          cs[i] = v.x;
-          sn[i] = v.y;
-        }
-      }
-      for (int h0 = ty; h0 < p.total_heads; h0 += kRotUnroll * p.by) {
-        T a[kRotUnroll][VEC], bb[HALF ? kRotUnroll : 1][VEC];
-        T *dst[kRotUnroll];
-#pragma unroll
-        for (int j = 0; j < kRotUnroll; ++j) {
-          const int h = h0 + j * p.by;
-          if (h >= p.total_heads) break;
-          const RotHeads &t = p.t[h >= p.t[0].heads ? 1 : 0];
-          const int hh = h >= p.t[0].heads ? h - p.t[0].heads : h;
-          const T *src = static_cast<const T *>(t.x) + b * t.xb + tok * t.xt + hh * t.xh + v0;
-          dst[j] = static_cast<T *>(t.y) + b * t.yb + tok * t.yt + hh * t.yh + v0;
-          IO::load(src, a[j]);
-          if constexpr (HALF) {
-            if (rotated) IO::load(src + pairs, bb[j]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kRotUnroll; ++j) {
-          const int h = h0 + j * p.by;
-          if (h >= p.total_heads) break;
-          if (rotated) {
-            if constexpr (HALF) {
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) {
-                const float x0 = to_f32<T>(a[j][i]), x1 = to_f32<T>(bb[j][i]);
-                a[j][i] = from_f32<T>(__fmaf_rn(x0, cs[i], -(x1 * sn[i])));
-                bb[j][i] = from_f32<T>(__fmaf_rn(x0, sn[i], x1 * cs[i]));
-              }
-              IO::store(dst[j] + pairs, bb[j]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < NP; ++i) {
-                const float x0 = to_f32<T>(a[j][2 * i]), x1 = to_f32<T>(a[j][2 * i + 1]);
-                a[j][2 * i] = from_f32<T>(__fmaf_rn(x0, cs[i], -(x1 * sn[i])));
-                a[j][2 * i + 1] = from_f32<T>(__fmaf_rn(x0, sn[i], x1 * cs[i]));
-              }
-            }
-          }
-          IO::store(dst[j], a[j]);
-        }
-      }
+    for (int i = 0; i < NP; ++i) {
+      const float2 v = f[i];
+      cs[i] = v.x;
+      sn[i] = v.y;
     }
+  }
+  for (int h0 = h_first;;) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int h = h0 + j * rows;
+      if (h >= p.total_heads) break;
+      T *dst = static_cast<T *>(p.t[h >= p.t[0].heads ? 1 : 0].y) + place(h, true);
+      if (rotated) {
+        if constexpr (HALF) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float x0 = to_f32<T>(va[j][i]), x1 = to_f32<T>(vb[j][i]);
+            va[j][i] = from_f32<T>(__fmaf_rn(x0, cs[i], -(x1 * sn[i])));
+            vb[j][i] = from_f32<T>(__fmaf_rn(x0, sn[i], x1 * cs[i]));
+          }
+          IO::store(dst + pairs, vb[j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const float x0 = to_f32<T>(va[j][2 * i]), x1 = to_f32<T>(va[j][2 * i + 1]);
+            va[j][2 * i] = from_f32<T>(__fmaf_rn(x0, cs[i], -(x1 * sn[i])));
+            va[j][2 * i + 1] = from_f32<T>(__fmaf_rn(x0, sn[i], x1 * cs[i]));
+          }
+        }
+      }
+      IO::store(dst, va[j]);
+    }
+    h0 += U * rows;
+    if (h0 >= p.total_heads) break;
+    load(h0);
   }
 }
 
