@@ -442,7 +442,8 @@ def make_grad(M, N, K, seed):
 GRAD_SHAPES = [
     (1, 8, 16), (1, 136, 128), (3, 4096, 4096), (16, 1000, 528), (17, 264, 144), (33, 520, 1040), (64, 256, 128),
     (129, 2056, 272), (300, 264, 256), (511, 1032, 2064), (700, 4096, 1024), (5, 13000, 256), (260, 24, 16),
-    (1300, 520, 4112),
+    (1300, 520, 4112), (297, 8, 32), (600, 40, 64), (900, 5000, 128), (310, 12288, 32), (333, 9000, 16),
+    (2500, 2064, 256),
 ]
 
 

@@ -974,18 +974,50 @@ size_t input_grad_head_bytes(int64_t M, int64_t N) {
          align256(static_cast<size_t>(M) * sizeof(float));
 }
 
+template <int V>
+int launch_quant_grad_stream(const uint16_t *dy, int64_t M, int64_t N, int64_t lddy, const float *s_w,
+                             int8_t *codes, float *s_g, const DeviceInfo &d, cudaStream_t stream) {
+  const int tpr = V == 1 ? static_cast<int>(N / 8) : kGradThreads;
+  const int rpi = kGradThreads / tpr;
+  const int64_t chunk_rows = static_cast<int64_t>(rpi) * kGradRows;
+  const int64_t chunks = cdiv(M, chunk_rows);
+  const int64_t slot = chunk_rows * N * 2;
+  const int64_t blocks = kGradBlocks<V>;  // sharing an SM
+  const int64_t room = d.max_smem_optin / blocks - 2048;
+  int64_t slots = (room - 3 * chunk_rows * 4) / slot;
+  if (slots > kGradMaxSlots) slots = kGradMaxSlots;
+  const int64_t grid = chunks < blocks * d.sms ? chunks : blocks * d.sms;
+  if (slots > cdiv(chunks, grid)) slots = cdiv(chunks, grid);
+  constexpr auto kernel = quant_grad_stream_kernel<V>;
+  int st = ensure_smem_limit<kernel>(static_cast<int>(room));
+  if (st != W8A8_OK) return st;
+  return launch_ex(true, kernel, dim3(static_cast<unsigned>(grid)), dim3(kGradThreads),
+                   static_cast<size_t>(slots * slot + 3 * chunk_rows * 4), stream, dy,
+                   static_cast<int>(M), static_cast<int>(N), lddy, s_w, codes, grad_code_stride(N), s_g,
+                   tpr, rpi, static_cast<int>(slots));
+}
+
 int launch_quant_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, const float *s_w,
-                      int8_t *codes, float *s_g, cudaStream_t stream) {
+                      int8_t *codes, float *s_g, const DeviceInfo &d, cudaStream_t stream) {
   const uint16_t *src = static_cast<const uint16_t *>(dy);
   const int64_t ldc = grad_code_stride(N);
   const dim3 grid(static_cast<unsigned>(M));
   const int n32 = static_cast<int>(N);
-  switch (cdiv(N / 8, 256)) {
-    case 1: return launch_ex(true, quant_grad_rows_kernel<1>, grid, dim3(256), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
-    case 2: return launch_ex(true, quant_grad_rows_kernel<2>, grid, dim3(256), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
-    case 3: case 4: return launch_ex(true, quant_grad_rows_kernel<4>, grid, dim3(256), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
-    case 5: case 6: return launch_ex(true, quant_grad_rows_kernel<6>, grid, dim3(256), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
-    default: return launch_ex(true, quant_grad_rows_kernel<0>, grid, dim3(256), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
+  const int64_t v = cdiv(N / 8, kGradThreads);
+  // The streaming kernel gives each SM whole chunks of rows; with fewer rows
+  // than two per SM a block per row spreads them wider.
+  if (v <= kGradMaxV && M >= 2 * d.sms) {
+    switch (v) {
+      case 1: return launch_quant_grad_stream<1>(src, M, N, lddy, s_w, codes, s_g, d, stream);
+      case 2: return launch_quant_grad_stream<2>(src, M, N, lddy, s_w, codes, s_g, d, stream);
+      default: return launch_quant_grad_stream<3>(src, M, N, lddy, s_w, codes, s_g, d, stream);
+    }
+  }
+  switch (v) {
+    case 1: return launch_ex(true, quant_grad_rows_kernel<1>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
+    case 2: return launch_ex(true, quant_grad_rows_kernel<2>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
+    case 3: return launch_ex(true, quant_grad_rows_kernel<3>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
+    default: return launch_ex(true, quant_grad_rows_kernel<0>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
   }
 }
 
@@ -1118,7 +1150,7 @@ int launch_rotary_t(RotParams &p, bool copy_rest, cudaStream_t stream) {
   const int pairs = p.rot / 2;
   p.rot_units = HALF ? pairs / VEC : p.rot / VEC;
   p.units = p.rot_units + (copy_rest ? (p.dim - p.rot) / VEC : 0);
-  const int threads = p.units <= 256 ? 256 : kRotThreads;
+  const int threads = p.units <= 32 ? 128 : (p.units <= 128 ? 256 : kRotThreads);
   p.bx = p.units;
   p.by = threads / p.bx;
   // Tokens per block: a divisor of the thread rows, with which the heads fill
@@ -1910,7 +1942,7 @@ int w8a8_linear_input_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, c
   // programmatic dependent
   st = clear_counters(split.counters, split.counters ? split_counter_bytes(plan) : 0, stream);
   if (st != W8A8_OK) return st;
-  st = launch_quant_grad(dy, M, N, lddy, s_w, codes, s_g, stream);
+  st = launch_quant_grad(dy, M, N, lddy, s_w, codes, s_g, *d, stream);
   if (st != W8A8_OK) return st;
   switch (plan.variant) {
     case W8A8_VARIANT_GEMM_PAIR:

@@ -658,10 +658,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
       ok = __all_sync(0xFFFFFFFFu, ok);
     }
     __syncthreads();
-    if (p.slabs > 1 && tid == 0 && ok) {  // this block has read the sample's entries
-      __threadfence();
+    // This block has read the sample's entries: their tags were compared before
+    // the barrier, so the loads are done and the mark needs no fence (which
+    // would hold the first warp back for a microsecond).
+    if (p.slabs > 1 && tid == 0 && ok)
       *reinterpret_cast<volatile unsigned long long *>(p.readers + static_cast<int64_t>(b) * p.slabs + slab) = p.tag;
-    }
     if (!BWD && slab == 0 && p.mean_out != nullptr && ok) {
       for (int g = tid; g < p.G; g += kNormThreads) {
         p.mean_out[static_cast<int64_t>(b) * p.G + g] = stat[g].x;
