@@ -951,13 +951,22 @@ int launch_swapab(const w8a8_plan &plan, const int8_t *q, const float *s_a, int6
 // Plan of the input gradient: rows M, output columns K, contraction N.  The
 // layer's plan for a [K, N] weight, without the variants that have no
 // MN-major form: the GEMV goes to the tensor-core small-M kernel, the
-// 64-column tiles to 128.
+// 64-column tiles to 128.  One more rule, from 51 shapes of 1-4352 rows (N
+// 4096-18432, K 2048-12288; graphs of rotating inputs): where the sum is 12288
+// or longer and few tiles have to walk it, CTA pairs share it out along N
+// (64 x 12288 x 4096: 26.9 us against 31.5 in 128-wide tiles; 512 x 18432 x
+// 2048: 45.0 against 54.0); from 32 pair tiles on they lose (400 x 12288 x
+// 4096: 39.5 against 37.6; 64 x 12288 x 8192: 36.0 against 32.2), as they do on
+// sums of 8192 (64 x 8192 x 4096: 25.1 against 22.4).
+constexpr int64_t kGradPairMinN = 12288, kGradPairMaxTiles = 24, kGradPairMinM = 33;
 int select_input_grad_plan(int64_t M, int64_t N, int64_t K, int32_t sms, int variant, int max_smem,
                            w8a8_plan *plan) {
   if (variant == W8A8_VARIANT_GEMV || variant == W8A8_VARIANT_GEMM_BN64)
     return W8A8_ERR_UNSUPPORTED_SHAPE;
   int st = select_plan(M, K, N, sms, variant, max_smem, plan);
   if (st != W8A8_OK || variant != W8A8_VARIANT_AUTO) return st;
+  if (N >= kGradPairMinN && M >= kGradPairMinM && sms >= 2 && cdiv(M, 256) * cdiv(K, 256) <= kGradPairMaxTiles)
+    return select_plan(M, K, N, sms, W8A8_VARIANT_GEMM_PAIR, max_smem, plan);
   if (plan->variant == W8A8_VARIANT_GEMV)
     return select_plan(M, K, N, sms, W8A8_VARIANT_GEMV_TC, max_smem, plan);
   if (plan->variant == W8A8_VARIANT_GEMM_BN64)
@@ -976,7 +985,8 @@ size_t input_grad_head_bytes(int64_t M, int64_t N) {
 
 template <int V>
 int launch_quant_grad_stream(const uint16_t *dy, int64_t M, int64_t N, int64_t lddy, const float *s_w,
-                             int8_t *codes, float *s_g, const DeviceInfo &d, cudaStream_t stream) {
+                             int8_t *codes, float *s_g, unsigned long long *counters, int n_counters,
+                             const DeviceInfo &d, cudaStream_t stream) {
   const int tpr = V == 1 ? static_cast<int>(N / 8) : kGradThreads;
   const int rpi = kGradThreads / tpr;
   const int64_t chunk_rows = static_cast<int64_t>(rpi) * kGradRows;
@@ -994,11 +1004,12 @@ int launch_quant_grad_stream(const uint16_t *dy, int64_t M, int64_t N, int64_t l
   return launch_ex(true, kernel, dim3(static_cast<unsigned>(grid)), dim3(kGradThreads),
                    static_cast<size_t>(slots * slot + 3 * chunk_rows * 4), stream, dy,
                    static_cast<int>(M), static_cast<int>(N), lddy, s_w, codes, grad_code_stride(N), s_g,
-                   tpr, rpi, static_cast<int>(slots));
+                   tpr, rpi, static_cast<int>(slots), counters, n_counters);
 }
 
 int launch_quant_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, const float *s_w,
-                      int8_t *codes, float *s_g, const DeviceInfo &d, cudaStream_t stream) {
+                      int8_t *codes, float *s_g, unsigned long long *counters, int n_counters,
+                      const DeviceInfo &d, cudaStream_t stream) {
   const uint16_t *src = static_cast<const uint16_t *>(dy);
   const int64_t ldc = grad_code_stride(N);
   const dim3 grid(static_cast<unsigned>(M));
@@ -1008,16 +1019,16 @@ int launch_quant_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, const 
   // than two per SM a block per row spreads them wider.
   if (v <= kGradMaxV && M >= 2 * d.sms) {
     switch (v) {
-      case 1: return launch_quant_grad_stream<1>(src, M, N, lddy, s_w, codes, s_g, d, stream);
-      case 2: return launch_quant_grad_stream<2>(src, M, N, lddy, s_w, codes, s_g, d, stream);
-      default: return launch_quant_grad_stream<3>(src, M, N, lddy, s_w, codes, s_g, d, stream);
+      case 1: return launch_quant_grad_stream<1>(src, M, N, lddy, s_w, codes, s_g, counters, n_counters, d, stream);
+      case 2: return launch_quant_grad_stream<2>(src, M, N, lddy, s_w, codes, s_g, counters, n_counters, d, stream);
+      default: return launch_quant_grad_stream<3>(src, M, N, lddy, s_w, codes, s_g, counters, n_counters, d, stream);
     }
   }
   switch (v) {
-    case 1: return launch_ex(true, quant_grad_rows_kernel<1>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
-    case 2: return launch_ex(true, quant_grad_rows_kernel<2>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
-    case 3: return launch_ex(true, quant_grad_rows_kernel<3>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
-    default: return launch_ex(true, quant_grad_rows_kernel<0>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g);
+    case 1: return launch_ex(true, quant_grad_rows_kernel<1>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g, counters, n_counters);
+    case 2: return launch_ex(true, quant_grad_rows_kernel<2>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g, counters, n_counters);
+    case 3: return launch_ex(true, quant_grad_rows_kernel<3>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g, counters, n_counters);
+    default: return launch_ex(true, quant_grad_rows_kernel<0>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g, counters, n_counters);
   }
 }
 
@@ -1938,11 +1949,9 @@ int w8a8_linear_input_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, c
   int8_t *codes = static_cast<int8_t *>(workspace);
   float *s_g = reinterpret_cast<float *>(codes + (head - align256(static_cast<size_t>(M) * sizeof(float))));
   const SplitRegion split = split_region(plan, codes + head, ws_bytes - head);
-  // cleared before the quantization kernel, so that the product stays its
-  // programmatic dependent
-  st = clear_counters(split.counters, split.counters ? split_counter_bytes(plan) : 0, stream);
-  if (st != W8A8_OK) return st;
-  st = launch_quant_grad(dy, M, N, lddy, s_w, codes, s_g, *d, stream);
+  // the quantization kernel clears the K split's counters on its way
+  const int n_counters = split.counters ? plan.split_tiles * kSlicesPerTile : 0;
+  st = launch_quant_grad(dy, M, N, lddy, s_w, codes, s_g, split.counters, n_counters, *d, stream);
   if (st != W8A8_OK) return st;
   switch (plan.variant) {
     case W8A8_VARIANT_GEMM_PAIR:

@@ -34,6 +34,14 @@ __device__ __forceinline__ void scale_vec8(uint4 v, const float *sw, float (&g)[
   g[6] = __fmul_rn(g[6], b.z); g[7] = __fmul_rn(g[7], b.w);
 }
 
+// The first block clears the arrival counters of the product that follows (its
+// epilogue reads them behind its own dependency wait): one launch less than a
+// memset ahead of this kernel, 3 us on its way.
+__device__ __forceinline__ void clear_split_counters(unsigned long long *counters, int n) {
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0ull;
+}
+
 __device__ __forceinline__ uint2 grad_codes8(const float (&g)[8], float s, float y, bool fast) {
   uint32_t c[8];
   if (fast) {
@@ -62,7 +70,7 @@ template <int V>
 __global__ void __launch_bounds__(kGradThreads)
     quant_grad_rows_kernel(const uint16_t *__restrict__ dy, int N, int64_t lddy,
                            const float *__restrict__ s_w, int8_t *__restrict__ codes, int64_t ldc,
-                           float *__restrict__ s_g) {
+                           float *__restrict__ s_g, unsigned long long *counters, int n_counters) {
   __shared__ uint32_t red[kGradWarps];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
@@ -71,6 +79,7 @@ __global__ void __launch_bounds__(kGradThreads)
   // the product that follows reads only Wq before its own dependency wait
   grid_dependents_launch();
   grid_dependency_wait();
+  clear_split_counters(counters, n_counters);
   uint4 v[V > 0 ? V : 1];
   float m = 0.0f;
   if constexpr (V > 0) {
@@ -147,7 +156,8 @@ template <int V>
 __global__ void __launch_bounds__(kGradThreads, kGradBlocks<V>)
     quant_grad_stream_kernel(const uint16_t *__restrict__ dy, int M, int N, int64_t lddy,
                              const float *__restrict__ s_w, int8_t *__restrict__ codes, int64_t ldc,
-                             float *__restrict__ s_g, int tpr, int rpi, int slots) {
+                             float *__restrict__ s_g, int tpr, int rpi, int slots,
+                             unsigned long long *counters, int n_counters) {
   extern __shared__ __align__(128) uint8_t grad_smem[];
   __shared__ uint64_t full[kGradMaxSlots], empty[kGradMaxSlots];
   __shared__ int abort_flag;
@@ -174,6 +184,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks<V>)
   // the product that follows reads only Wq before its own dependency wait
   grid_dependents_launch();
   grid_dependency_wait();
+  clear_split_counters(counters, n_counters);
   float2 sw[V][4];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
