@@ -247,6 +247,10 @@ NORM_CASES = [
     ((1, 70000, 16), 2, True, torch.bfloat16, "same", 0.0),
     ((1, 5000, 128), 32, False, torch.float32, "same", 1000.0),     # a mean far from zero
     ((2, 4, 3, 5, 2, 48), 6, True, torch.float16, "same", 0.0),
+    ((1, 2500, 256), 256, True, torch.bfloat16, "same", 2.0),       # many groups, many blocks
+    ((1, 1300, 1024), 512, False, torch.float16, "same", 0.0),
+    ((1, 700, 2048), 2048, True, torch.float32, "same", -3.0),
+    ((1, 30000, 64), 64, True, torch.bfloat16, "same", 0.0),
 ]
 
 

@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
       // per channel over the rows, to global memory; weighted in place
       for (int ch = tid; ch < p.C; ch += kNormThreads) {
         float2 t = region[ch];
-#pragma unroll 8
+#pragma unroll 4
         for (int r = 1; r < p.rpi; ++r) {
           t.x += region[r * p.C + ch].x;
           t.y += region[r * p.C + ch].y;
@@ -541,6 +541,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
       return BWD ? make_float2(t.x / count, t.y / count) : make_float2(t.x, rsqrtf(t.y / count + p.eps));
     };
     const int gstep = kNormThreads >> p.group_shift;
+#pragma unroll 1
     for (int g0 = 0; g0 < p.G; g0 += gstep) {  // whole warps stay together
       const int g = g0 + (tid >> p.group_shift);
       float2 mine = make_float2(0.0f, 0.0f);
@@ -594,64 +595,66 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     }
     // ---- the sample's groups, from every block's entry
     if (p.slabs > 1) {
-      constexpr int E = 10;  // entries a lane keeps in registers
+      constexpr int E = 5;  // entries a lane has under way at once
       const int part = p.slab_part, extra = p.slab_extra;
+#pragma unroll 1
       for (int g0 = 0; g0 < p.G; g0 += gstep) {
         const int g = g0 + (tid >> p.group_shift);
         const uint4 *e = entries + static_cast<int64_t>(g) * p.slabs;
-        float2 v[E], t = make_float2(0.0f, 0.0f);
-        if (p.slabs <= E * lanes) {
+        float2 t = make_float2(0.0f, 0.0f);  // this lane's mean and deviations, or sums
+        float have = 0.0f;                   // pixels they stand for
+#pragma unroll 1
+        for (int j0 = 0; j0 < p.slabs; j0 += E * lanes) {
+          float2 v[E];
           unsigned long long tag[E];
 #pragma unroll
-          for (int u = 0; u < E; ++u) {  // all loads under way at once
-            const int j = sub + lanes * u;
+          for (int u = 0; u < E; ++u) {
+            const int j = j0 + sub + lanes * u;
             tag[u] = p.tag;
             v[u] = make_float2(0.0f, 0.0f);
             if (j < p.slabs && g < p.G) tag[u] = entry_load(e + j, v[u]);
           }
 #pragma unroll
           for (int u = 0; u < E; ++u) {
-            if (tag[u] != p.tag && ok) ok = entry_wait(e + sub + lanes * u, p.tag, v[u], &abort_flag);
+            if (tag[u] != p.tag && ok) ok = entry_wait(e + j0 + sub + lanes * u, p.tag, v[u], &abort_flag);
           }
-#pragma unroll
-          for (int u = 0; u < E; ++u) {
-            const int j = sub + lanes * u;
-            const float pix = j < p.slabs ? static_cast<float>(part + (j < extra ? 1 : 0)) : 0.0f;
-            t.x += BWD ? v[u].x : pix * v[u].x;
-            if (BWD) t.y += v[u].y;
-          }
-          t.x = group_sum(t.x);
-          if constexpr (!BWD) {
-            t.x /= static_cast<float>(p.S);
+          if constexpr (BWD) {
 #pragma unroll
             for (int u = 0; u < E; ++u) {
-              const int j = sub + lanes * u;
-              const float pix = j < p.slabs ? static_cast<float>(part + (j < extra ? 1 : 0)) : 0.0f;
-              const float dd = v[u].x - t.x;
-              t.y += v[u].y + pix * c * dd * dd;
+              t.x += v[u].x;
+              t.y += v[u].y;
             }
-          }
-          t.y = group_sum(t.y);
-        } else {  // many groups: the entries are read twice
-          if (g < p.G) {
-            for (int j = sub; j < p.slabs && ok; j += lanes) {
-              ok = entry_wait(e + j, p.tag, v[0], &abort_flag);
-              t.x += BWD ? v[0].x : static_cast<float>(part + (j < extra ? 1 : 0)) * v[0].x;
-              if (BWD) t.y += v[0].y;
+          } else {
+            float pix = 0.0f, mean = 0.0f, dev = 0.0f;
+#pragma unroll
+            for (int u = 0; u < E; ++u) {
+              const int j = j0 + sub + lanes * u;
+              const float n = j < p.slabs ? static_cast<float>(part + (j < extra ? 1 : 0)) : 0.0f;
+              pix += n;
+              mean += n * v[u].x;
             }
-          }
-          t.x = group_sum(t.x);
-          if constexpr (!BWD) {
-            t.x /= static_cast<float>(p.S);
-            if (g < p.G) {
-              for (int j = sub; j < p.slabs && ok; j += lanes) {
-                entry_load(e + j, v[0]);
-                const float dd = v[0].x - t.x;
-                t.y += v[0].y + static_cast<float>(part + (j < extra ? 1 : 0)) * c * dd * dd;
+            if (pix > 0.0f) {
+              mean /= pix;
+#pragma unroll
+              for (int u = 0; u < E; ++u) {
+                const int j = j0 + sub + lanes * u;
+                const float n = j < p.slabs ? static_cast<float>(part + (j < extra ? 1 : 0)) : 0.0f;
+                const float dd = v[u].x - mean;
+                dev += v[u].y + n * c * dd * dd;
               }
+              const float delta = mean - t.x, share = pix / (have + pix);
+              t.y += dev + delta * delta * share * have * c;
+              t.x += delta * share;
+              have += pix;
             }
           }
-          t.y = group_sum(t.y);
+        }
+        if constexpr (BWD) {
+          t = make_float2(group_sum(t.x), group_sum(t.y));
+        } else {
+          const float mean = group_sum(have * t.x) / static_cast<float>(p.S);
+          const float dd = t.x - mean;
+          t = make_float2(mean, group_sum(t.y + have * c * dd * dd));
         }
         if (sub == 0 && g < p.G) stat[g] = finish(t);
       }
