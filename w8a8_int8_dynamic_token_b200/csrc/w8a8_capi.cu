@@ -1293,11 +1293,11 @@ int launch_norm_mode(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaS
   const size_t region =
       MODE == kNormBackward
           ? static_cast<size_t>(p.C) * sizeof(float2) * (p.rpi > 2 ? p.rpi : 2)
-          : (static_cast<size_t>(p.rpi) * p.tpr * (kNormVec<T> / p.run) + p.G) * sizeof(float2) +
-                (MODE == kNormQuant ? 3 * static_cast<size_t>(c.rows) * sizeof(uint32_t) : 0);
+          : (static_cast<size_t>(p.rpi) * p.tpr * (kNormVec<T> / p.run) + p.G) * sizeof(float2);
+  const int64_t maxima = MODE == kNormQuant ? c.rows * static_cast<int64_t>(sizeof(uint32_t)) : 0;  // a slot's
   p.chunk_bytes = c.rows * p.C * static_cast<int32_t>(sizeof(T));
   const int64_t slot = static_cast<int64_t>(p.chunk_bytes) * (MODE == kNormBackward ? 2 : 1);
-  int64_t slots = (d.max_smem_optin - 1024 - static_cast<int64_t>(region)) / slot;
+  int64_t slots = (d.max_smem_optin - 1024 - static_cast<int64_t>(region)) / (slot + maxima);
   const int64_t chunks = cdiv(cdiv(p.S, c.slabs), c.rows);
   if (slots > kNormMaxSlots) slots = kNormMaxSlots;
   if (slots > chunks) slots = chunks;
@@ -1311,7 +1311,7 @@ int launch_norm_mode(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaS
   attr.val.cooperative = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(c.slabs), static_cast<unsigned>(c.teams));
   cfg.blockDim = dim3(kNormThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(slots * slot) + region;
+  cfg.dynamicSmemBytes = static_cast<size_t>(slots * (slot + maxima)) + region;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = c.slabs > 1 ? 1 : 0;

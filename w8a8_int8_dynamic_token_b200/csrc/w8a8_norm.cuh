@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
   __shared__ int abort_flag;
   const int NS = p.slots;
   const int slot_bytes = p.chunk_bytes * (BWD ? 2 : 1);
-  // [slots][x rows, dy rows] | the statistics' region | row maxima (int8 form)
+  // [slots][x rows, dy rows] | the statistics' region | [slots] row maxima (int8 form)
   float2 *region = reinterpret_cast<float2 *>(norm_smem + NS * slot_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunk_rows = p.rpi * K;
@@ -691,151 +691,157 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
         }
       });
     }
-    uint32_t *row_max = reinterpret_cast<uint32_t *>(stat + p.G);  // int8 form: [3][chunk_rows]
-    if constexpr (MODE == kNormQuant) {
-      for (int i = tid; i < 3 * chunk_rows; i += kNormThreads) row_max[i] = 0u;
-      __syncthreads();
-    }
-    int turn = 0;
-    const bool one_row = (p.tpr & 31) == 0;        // a warp's threads share a row
-    const int first = __shfl_sync(0xFFFFFFFFu, row, 0);
-    // where this thread's first row of a chunk goes, from the last chunk down
-    uint8_t *dst = nullptr;
-    int64_t dst_row = 0, dst_chunk = 0;
-    int64_t pix = static_cast<int64_t>(b) * p.S + lo + static_cast<int64_t>(chunks - 1) * chunk_rows + row;
-    if constexpr (MODE != kNormQuant) {
-      dst = static_cast<uint8_t *>(p.y) +
-            (b * p.yb + (lo + static_cast<int64_t>(chunks - 1) * chunk_rows + row) * p.ys + vec * V) *
-                static_cast<int64_t>(sizeof(T));
-      dst_row = p.rpi * p.ys * static_cast<int64_t>(sizeof(T));
-      dst_chunk = dst_row * K;
-    }
     // K rows (`all`), or nb of them: no branch between rows where there are K,
-    // so that their work interleaves
-    auto apply = [&](const uint8_t *src, int nb, auto all) {
-      constexpr bool ALL = decltype(all)::value;
-      // the int8 form's rows meet at a barrier, so its idle threads come too
-      const bool here = MODE != kNormQuant || live;
-      float2 z[K][H];
+    // so that their work interleaves.  y of this thread's rows of a chunk:
+    auto values = [&](const uint8_t *src, int k, float2 (&z)[H]) __attribute__((always_inline)) {
+      const uint4 xv = *reinterpret_cast<const uint4 *>(src + k * row_step);
+      if constexpr (BWD) {
+        float2 xh[H];
+        grad_vec(xv, *reinterpret_cast<const uint4 *>(src + p.chunk_bytes + k * row_step), xh, z);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (here && (ALL || k < nb)) {
-          const uint4 xv = *reinterpret_cast<const uint4 *>(src + k * row_step);
-          if constexpr (BWD) {
-            float2 xh[H];
-            grad_vec(xv, *reinterpret_cast<const uint4 *>(src + p.chunk_bytes + k * row_step), xh, z[k]);
+        for (int h = 0; h < H; ++h) z[h] = fma2_rn(z[h], k1[h], fma2_rn(xh[h], k3[h], k2[h]));
+      } else {
+        Pairs<T>::get(xv, z);
 #pragma unroll
-            for (int h = 0; h < H; ++h)
-              z[k][h] = fma2_rn(z[k][h], k1[h], fma2_rn(xh[h], k3[h], k2[h]));
-          } else {
-            Pairs<T>::get(xv, z[k]);
+        for (int h = 0; h < H; ++h) {
+          z[h] = fma2_rn(add2_rn(z[h], k3[h]), k1[h], k2[h]);
+          if constexpr (SILU) z[h] = mul2_rn(z[h], sigmoid2(z[h]));
+        }
+      }
+    };
+    if constexpr (MODE == kNormQuant) {
+      // int8 rows.  Windows of up to a ring of chunks: first every row's
+      // maximum, then, behind one barrier, the codes (y is formed twice: a
+      // barrier per chunk, with y kept, took 10 us where this takes 6, at 2 x
+      // 4096 x 1280).
+      uint32_t *row_max = reinterpret_cast<uint32_t *>(stat + p.G);  // [slots][chunk_rows]
+      const bool one_row = (p.tpr & 31) == 0;  // a warp's threads share a row
+      const int first = __shfl_sync(0xFFFFFFFFu, row, 0);
+      // One maximum per warp and row goes to shared memory (a warp holds one or
+      // two rows, or several narrow ones; maxima do not depend on the order).
+      auto maxima = [&](const uint8_t *src, uint32_t *mx, int nb) {
+        uint32_t mb[K];
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-              z[k][h] = fma2_rn(add2_rn(z[k][h], k3[h]), k1[h], k2[h]);
-              if constexpr (SILU) z[k][h] = mul2_rn(z[k][h], sigmoid2(z[k][h]));
+        for (int k = 0; k < K; ++k) {
+          float m = 0.0f;
+          if (k < nb) {
+            float2 z[H];
+            values(src, k, z);
+#pragma unroll
+            for (int h = 0; h < H; ++h) m = fmaxf(m, fmaxf(fabsf(z[h].x), fabsf(z[h].y)));
+          }
+          mb[k] = __float_as_uint(m);
+        }
+        if (one_row) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) mb[k] = __reduce_max_sync(0xFFFFFFFFu, mb[k]);
+          if (lane == 0 && live) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) atomicMax(mx + row + k * p.rpi, mb[k]);
+          }
+        } else if (p.tpr > 32) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, row == first ? 0u : mb[k]);
+            const uint32_t m0 = __reduce_max_sync(0xFFFFFFFFu, row == first ? mb[k] : 0u);
+            if (lane == 0) {
+              if (first < p.rpi) atomicMax(mx + first + k * p.rpi, m0);
+              if (first + 1 < p.rpi) atomicMax(mx + first + 1 + k * p.rpi, m1);
             }
           }
-        }
-      }
-      if constexpr (MODE != kNormQuant) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-          if (ALL || k < nb) *reinterpret_cast<uint4 *>(dst + k * dst_row) = Pairs<T>::put(z[k]);
-        return;
-      }
-      // int8 rows.  A row's threads are neighbours: a warp holds one or two
-      // rows, or, of narrow rows, several.  One maximum per warp and row goes
-      // to shared memory (maxima do not depend on the order).
-      uint32_t *mx = row_max + turn * chunk_rows;
-      uint32_t mb[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        float m = 0.0f;
-        if (here && (ALL || k < nb)) {
-#pragma unroll
-          for (int h = 0; h < H; ++h) m = fmaxf(m, fmaxf(fabsf(z[k][h].x), fabsf(z[k][h].y)));
-        }
-        mb[k] = __float_as_uint(m);
-      }
-      if (one_row) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) mb[k] = __reduce_max_sync(0xFFFFFFFFu, mb[k]);
-        if (lane == 0 && live) {
+        } else if (live) {
 #pragma unroll
           for (int k = 0; k < K; ++k) atomicMax(mx + row + k * p.rpi, mb[k]);
         }
-      } else if (p.tpr > 32) {
-        uint32_t m1[K];
+      };
+      auto codes = [&](const uint8_t *src, const uint32_t *mx, int nb, int64_t pix) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          m1[k] = __reduce_max_sync(0xFFFFFFFFu, row == first ? 0u : mb[k]);
-          mb[k] = __reduce_max_sync(0xFFFFFFFFu, row == first ? mb[k] : 0u);
-        }
-        if (lane == 0) {
+          if (k < nb) {
+            float2 z[H];
+            values(src, k, z);
+            // rint(y * (127 / amax)) in one fused step: y is a rounded fp32
+            // value already, so a quotient off by 2^-22 moves a code only
+            // where y is that close to a tie; the scale is the IEEE quotient.
+            // Next to the subnormals, where 127 / amax leaves fp32, divide.
+            const float amax = __uint_as_float(mx[row + k * p.rpi]);
+            uint32_t code[V];
+            if (amax >= 1e-30f) {
+              const float r = __fdividef(127.0f, amax);
 #pragma unroll
-          for (int k = 0; k < K; ++k) {
-            if (first < p.rpi) atomicMax(mx + first + k * p.rpi, mb[k]);
-            if (first + 1 < p.rpi) atomicMax(mx + first + 1 + k * p.rpi, m1[k]);
-          }
-        }
-      } else if (live) {
+              for (int h = 0; h < H; ++h) {
+                const float2 t = fma2_rn(z[h], make_float2(r, r), make_float2(kRintMagic, kRintMagic));
+                code[2 * h] = __float_as_uint(t.x);
+                code[2 * h + 1] = __float_as_uint(t.y);
+              }
+            } else {
+              const float sc = __fdiv_rn(amax, 127.0f);
 #pragma unroll
-        for (int k = 0; k < K; ++k) atomicMax(mx + row + k * p.rpi, mb[k]);
-      }
-      __syncthreads();
-      // the maxima of two chunks ago are no longer read: clear them for the
-      // chunk after the next
-      uint32_t *old = row_max + (turn == 0 ? 2 : turn - 1) * chunk_rows;
-      for (int r = tid; r < chunk_rows; r += kNormThreads) old[r] = 0u;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (here && (ALL || k < nb)) {
-          // rint(y * (127 / amax)) in one fused step: y is a rounded fp32
-          // value already, so a quotient off by 2^-22 moves a code only where
-          // y is that close to a tie; the scale is the IEEE quotient.  Next to
-          // the subnormals, where 127 / amax leaves fp32, divide.
-          const float amax = __uint_as_float(mx[row + k * p.rpi]);
-          uint32_t code[V];
-          if (amax >= 1e-30f) {
-            const float r = __fdividef(127.0f, amax);
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-              const float2 t = fma2_rn(z[k][h], make_float2(r, r), make_float2(kRintMagic, kRintMagic));
-              code[2 * h] = __float_as_uint(t.x);
-              code[2 * h + 1] = __float_as_uint(t.y);
+              for (int h = 0; h < H; ++h) {
+                code[2 * h] = sc == 0.0f ? 0u : quant_exact(z[h].x, sc);
+                code[2 * h + 1] = sc == 0.0f ? 0u : quant_exact(z[h].y, sc);
+              }
             }
-          } else {
-            const float sc = __fdiv_rn(amax, 127.0f);
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-              code[2 * h] = sc == 0.0f ? 0u : quant_exact(z[k][h].x, sc);
-              code[2 * h + 1] = sc == 0.0f ? 0u : quant_exact(z[k][h].y, sc);
-            }
-          }
-          if constexpr (V == 8) {
+            static_assert(V == 8, "int8 rows are made of bf16 activations");
             if (ok) {
               *reinterpret_cast<uint2 *>(p.q + (pix + k * p.rpi) * p.C + vec * V) = pack_codes(code);
               if (vec == 0) p.s_q[pix + k * p.rpi] = __fdiv_rn(amax, 127.0f);
             }
           }
         }
+      };
+      for (int top = chunks - 1; top >= 0; top -= NS) {
+        const int low = top - NS + 1 < 0 ? 0 : top - NS + 1;
+        __syncthreads();  // the window before is done with the maxima
+        for (int i = tid; i < NS * chunk_rows; i += kNormThreads) row_max[i] = 0u;
+        __syncthreads();
+        int s = slot;
+        for (int i = top; i >= low; --i) {
+          if (i < chunks - NS) arrive_full(s);
+          maxima(norm_smem + s * slot_bytes + offset, row_max + s * chunk_rows,
+                 i == chunks - 1 ? last_nb : (live ? K : 0));
+          s = s == 0 ? NS - 1 : s - 1;
+        }
+        __syncthreads();
+        for (int i = top; i >= low; --i) {
+          if (warp == 0 && i + 1 < chunks && i + 1 >= NS) fill(b, i + 1 - NS, slot + 1 == NS ? 0 : slot + 1);
+          codes(norm_smem + slot * slot_bytes + offset, row_max + slot * chunk_rows,
+                i == chunks - 1 ? last_nb : (live ? K : 0),
+                static_cast<int64_t>(b) * p.S + lo + static_cast<int64_t>(i) * chunk_rows + row);
+          release(slot);
+          slot = slot == 0 ? NS - 1 : slot - 1;
+        }
       }
-      turn = turn == 2 ? 0 : turn + 1;
-    };
-    for (int i = chunks - 1; i >= 0; --i) {
-      if (i < chunks - NS) arrive_full(slot);
-      if (warp == 0 && i + 1 < chunks && i + 1 >= NS) fill(b, i + 1 - NS, slot + 1 == NS ? 0 : slot + 1);
-      const uint8_t *src = norm_smem + slot * slot_bytes + offset;
-      // the int8 form's rows meet at a barrier: every thread takes part
-      if (i < chunks - 1 ? (live || MODE == kNormQuant) : last_nb == K && MODE != kNormQuant) {
-        if (ok || MODE == kNormQuant) apply(src, K, std::true_type{});
-      } else if (i == chunks - 1 && (last_nb > 0 || MODE == kNormQuant)) {
-        if (ok || MODE == kNormQuant) apply(src, last_nb, std::false_type{});
+    } else {
+      // where this thread's first row of a chunk goes, from the last chunk down
+      uint8_t *dst = static_cast<uint8_t *>(p.y) +
+                     (b * p.yb + (lo + static_cast<int64_t>(chunks - 1) * chunk_rows + row) * p.ys + vec * V) *
+                         static_cast<int64_t>(sizeof(T));
+      const int64_t dst_row = p.rpi * p.ys * static_cast<int64_t>(sizeof(T));
+      const int64_t dst_chunk = dst_row * K;
+      auto apply = [&](const uint8_t *src, int nb, auto all) {
+        constexpr bool ALL = decltype(all)::value;
+        float2 z[K][H];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (ALL || k < nb) values(src, k, z[k]);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (ALL || k < nb) *reinterpret_cast<uint4 *>(dst + k * dst_row) = Pairs<T>::put(z[k]);
+      };
+      for (int i = chunks - 1; i >= 0; --i) {
+        if (i < chunks - NS) arrive_full(slot);
+        if (warp == 0 && i + 1 < chunks && i + 1 >= NS) fill(b, i + 1 - NS, slot + 1 == NS ? 0 : slot + 1);
+        const uint8_t *src = norm_smem + slot * slot_bytes + offset;
+        if (i < chunks - 1 ? live : last_nb == K) {
+          if (ok) apply(src, K, std::true_type{});
+        } else if (i == chunks - 1 && last_nb > 0) {
+          if (ok) apply(src, last_nb, std::false_type{});
+        }
+        release(slot);
+        slot = slot == 0 ? NS - 1 : slot - 1;
+        dst -= dst_chunk;
       }
-      release(slot);
-      slot = slot == 0 ? NS - 1 : slot - 1;
-      dst -= dst_chunk;
-      pix -= chunk_rows;
     }
     if (p.slabs > 1 && slab == 0 && ok) {
       // once every block has read the sample's entries: their tags go
