@@ -420,6 +420,88 @@ def test_group_norm_gradient_against_differences(silu):
         assert abs(got - diff) <= scale * (100 * U + 10 * h * h)
 
 
+# Slabs longer than a block's ring: the second pass reads chunks again, in
+# place too, adjacent rows and strided ones.
+@pytest.mark.parametrize("shape,groups,dtype,pad", [
+    ((1, 130001, 128), 32, torch.bfloat16, 0), ((1, 130001, 128), 32, torch.bfloat16, 16),
+    ((3, 20011, 320), 32, torch.float32, 0), ((2, 3001, 4096), 32, torch.float16, 0),
+])
+def test_group_norm_longer_than_the_ring(shape, groups, dtype, pad):
+    Bn, S, C = shape
+    wide = torch.zeros((Bn, S, C + pad), dtype=dtype, device="cuda")
+    x = wide[..., :C]
+    x.copy_(torch.randn(shape, generator=torch.Generator("cuda").manual_seed(3), device="cuda") + 1.5)
+    w, b = (1 + 0.2 * torch.randn(C, generator=gen(4))).cuda(), (0.2 * torch.randn(C, generator=gen(5))).cuda()
+    xg = x.double().reshape(Bn, S, groups, C // groups)
+    m64 = xg.mean((1, 3))
+    r64 = 1 / torch.sqrt(((xg - m64[:, None, :, None]) ** 2).mean((1, 3)) + 1e-5)
+    xh = ((xg - m64[:, None, :, None]) * r64[:, None, :, None]).reshape(shape)
+    z = xh * w.double() + b.double()
+    gate = torch.sigmoid(z)
+    n = chain(S, C)
+    slack = 1.1 * U * (n * (1 + xh.abs() + (m64.abs() * r64).max()) * w.double().abs() + 4 * b.double().abs()) + \
+        z.abs() * gate * (6 + 1.2 * z.abs()) * 2 * U
+    y, mean, rstd = w8a8.group_norm(x, groups, w, b, activation="silu", return_stats=True)
+    close(y, (z * gate).cpu(), slack.cpu(), "y")
+    close(mean, m64.cpu(), (n * U * (m64.abs() + 1 / r64)).cpu(), "mean")
+    if dtype == torch.bfloat16:
+        q, s = w8a8.group_norm_quant(x, groups, w, b, activation="silu")
+        qs = q.double() * s.double()[:, None]
+        y64 = (z * gate).view(-1, C)
+        assert ((qs - y64).abs() <= s.double()[:, None] * (0.5 + 127 * 2 * U) + slack.view(-1, C)).all()
+    # gradient, against the formula on the device in 64 bits
+    dy = torch.randn(shape, generator=torch.Generator("cuda").manual_seed(6), device="cuda").to(dtype)
+    dx, dw, db = w8a8.group_norm_backward(dy, x, mean, rstd, w, b, activation="silu")
+    dz = dy.double() * gate * (1 + z * (1 - gate))
+    wdz = (dz * w.double()).view(xg.shape)
+    xhg = xh.view(xg.shape)
+    c1, c2 = wdz.mean((1, 3), keepdim=True), (wdz * xhg).mean((1, 3), keepdim=True)
+    want = (r64[:, None, :, None] * (wdz - c1 - xhg * c2)).reshape(shape)
+    # every term's fp32 roundings: the statistics' n U, the derivative's some
+    # 30 (1 + |z|), on |w dz|, its means and their products
+    part = r64[:, None, :, None] * (wdz.abs() + wdz.abs().mean((1, 3), keepdim=True) * (1 + xhg.abs()))
+    zz = (1 + z.abs().view(xg.shape)) * (1 + (m64.abs() * r64)[:, None, :, None])
+    tol = (part * (n + 60 * zz) * U + r64[:, None, :, None] * dy.double().view(xg.shape).abs() * 60 * zz * U).reshape(shape)
+    close(dx, want.cpu(), tol.cpu(), "dx")
+    sw = (dz * xh).abs().sum((0, 1)) + (dy.double().abs() * xh.abs() + dz.abs()).sum((0, 1))
+    close(dw, (dz * xh).sum((0, 1)).cpu(), ((n + 200) * U * sw).cpu(), "dweight")
+    close(db, dz.sum((0, 1)).cpu(), ((n + 200) * U * (dz.abs() + dy.double().abs()).sum((0, 1))).cpu(), "dbias")
+    again = x.clone() if pad == 0 else x
+    out = w8a8.group_norm(again, groups, w, b, activation="silu", out=again)
+    assert out is again and torch.equal(out, y)
+    if pad:
+        assert (wide[..., C:] == 0).all()
+
+
+@pytest.mark.parametrize("fill", [0x00, 0xFF, 0x5A])
+def test_group_norm_workspace_contents_do_not_matter(fill):
+    x, w, b, (xd, wd, bd) = make_norm((2, 3000, 64), torch.bfloat16, "same", 0.0)
+    want = w8a8.group_norm(xd, 8, wd, bd)
+    need = max(w8a8.group_norm_workspace_size(2, 3000, 64, 8), w8a8.group_norm_workspace_size(2, 3000, 64, 8, torch.bfloat16, True),
+               w8a8.group_norm_workspace_size(1, 900, 64, 16))
+    ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+    for _ in range(3):  # one workspace, other shapes and forms in between
+        assert torch.equal(w8a8.group_norm(xd, 8, wd, bd, workspace=ws), want)
+        w8a8.group_norm(xd[:1, :900], 16, wd, bd, workspace=ws)
+        q, s, mean, rstd = w8a8.group_norm_quant(xd, 8, wd, bd, return_stats=True, workspace=ws)
+        w8a8.group_norm_backward(xd, xd, mean, rstd, wd, bd, workspace=ws)
+
+
+def test_group_norm_on_two_streams_at_once():
+    jobs = []
+    for i, shape in enumerate([(1, 4096, 320), (2, 2000, 512)]):
+        x, w, b, dev = make_norm(shape, torch.bfloat16, "same", 0.0, seed=40 + i)
+        jobs.append((dev, w8a8.group_norm(dev[0], 32, dev[1], dev[2], activation="silu"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, ((x, w, b), _, s) in enumerate(jobs):
+            got[i].append(w8a8.group_norm(x, 32, w, b, activation="silu", stream=s))
+    torch.cuda.synchronize()
+    for (_, want, _), ys in zip(jobs, got):
+        assert all(torch.equal(y, want) for y in ys)
+
+
 # ----------------------------------------------------------------- input gradient
 
 def input_grad_ref(dy, Wq, s_w):
@@ -500,6 +582,44 @@ def test_linear_input_grad_against_the_unrounded_product():
     diff = (fwd(v) - fwd(-v)) / 2
     tol = ((slack + rounding(full.abs() + slack, torch.bfloat16)) * v.abs()).sum()
     assert abs((got.cpu().double() * v).sum() - diff) <= tol
+
+
+@pytest.mark.parametrize("M,N,K", [(600, 12288, 2064), (40, 264, 512), (320, 4096, 256)])
+def test_linear_input_grad_workspace_contents_do_not_matter(M, N, K):
+    dy, Wq, s_w = make_grad(M, N, K, 25)
+    want = input_grad_ref(dy, Wq, s_w)[0]
+    dyd, Wd, sd = dy.cuda(), Wq.cuda(), s_w.cuda()
+    need = w8a8.input_grad_workspace_size(M, N, K)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    outs = [w8a8.linear_input_grad(dyd, Wd, sd, workspace=ws) for _ in range(3)]
+    outs.append(w8a8.linear_input_grad(dyd, Wd, sd, workspace=ws[:((M * ((N + 15) // 16 * 16) + 255) // 256 + (4 * M + 255) // 256) * 256]))
+    for o in outs:  # the last one without the K split's region
+        assert torch.equal(o.cpu(), want)
+
+
+def test_linear_input_grad_right_after_quantize_weights():
+    # the channel scales and codes are written by the launch just before
+    g = gen(26)
+    dy = (torch.randn((48, 1024), generator=g) * 1e-3).bfloat16().cuda()
+    for i in range(8):
+        W = (torch.randn((1024, 2048), generator=g) * (i + 1)).bfloat16().cuda()
+        torch.cuda.synchronize()
+        Wq, s_w = w8a8.quantize_weights(W)
+        got = w8a8.linear_input_grad(dy, Wq, s_w)
+        assert torch.equal(got.cpu(), input_grad_ref(dy.cpu(), Wq.cpu(), s_w.cpu())[0])
+
+
+def test_linear_input_grad_extreme_scales():
+    # products next to the subnormals and next to the largest numbers: the
+    # codes take the dividing path
+    dy, Wq, s_w = make_grad(300, 64, 48, 27)
+    scale = torch.ones(300)
+    scale[::3], scale[1::3] = 1e-36, 1e36
+    dy = (dy.float() * scale[:, None]).bfloat16()
+    got = w8a8.linear_input_grad(dy.cuda(), Wq.cuda(), s_w.cuda())
+    assert torch.equal(got.cpu(), input_grad_ref(dy, Wq, s_w)[0])
+    few = w8a8.linear_input_grad(dy[:30].cuda(), Wq.cuda(), s_w.cuda())
+    assert torch.equal(few.cpu(), got[:30].cpu())
 
 
 # ----------------------------------------------------------------- together
