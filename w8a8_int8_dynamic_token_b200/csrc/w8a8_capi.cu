@@ -983,30 +983,6 @@ size_t input_grad_head_bytes(int64_t M, int64_t N) {
          align256(static_cast<size_t>(M) * sizeof(float));
 }
 
-template <int V>
-int launch_quant_grad_stream(const uint16_t *dy, int64_t M, int64_t N, int64_t lddy, const float *s_w,
-                             int8_t *codes, float *s_g, unsigned long long *counters, int n_counters,
-                             const DeviceInfo &d, cudaStream_t stream) {
-  const int tpr = V == 1 ? static_cast<int>(N / 8) : kGradThreads;
-  const int rpi = kGradThreads / tpr;
-  const int64_t chunk_rows = static_cast<int64_t>(rpi) * kGradRows;
-  const int64_t chunks = cdiv(M, chunk_rows);
-  const int64_t slot = chunk_rows * N * 2;
-  const int64_t blocks = kGradBlocks<V>;  // sharing an SM
-  const int64_t room = d.max_smem_optin / blocks - 2048;
-  int64_t slots = (room - 3 * chunk_rows * 4) / slot;
-  if (slots > kGradMaxSlots) slots = kGradMaxSlots;
-  const int64_t grid = chunks < blocks * d.sms ? chunks : blocks * d.sms;
-  if (slots > cdiv(chunks, grid)) slots = cdiv(chunks, grid);
-  constexpr auto kernel = quant_grad_stream_kernel<V>;
-  int st = ensure_smem_limit<kernel>(static_cast<int>(room));
-  if (st != W8A8_OK) return st;
-  return launch_ex(true, kernel, dim3(static_cast<unsigned>(grid)), dim3(kGradThreads),
-                   static_cast<size_t>(slots * slot + 3 * chunk_rows * 4), stream, dy,
-                   static_cast<int>(M), static_cast<int>(N), lddy, s_w, codes, grad_code_stride(N), s_g,
-                   tpr, rpi, static_cast<int>(slots), counters, n_counters);
-}
-
 int launch_quant_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, const float *s_w,
                       int8_t *codes, float *s_g, unsigned long long *counters, int n_counters,
                       const DeviceInfo &d, cudaStream_t stream) {
@@ -1014,16 +990,21 @@ int launch_quant_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, const 
   const int64_t ldc = grad_code_stride(N);
   const dim3 grid(static_cast<unsigned>(M));
   const int n32 = static_cast<int>(N);
-  const int64_t v = cdiv(N / 8, kGradThreads);
-  // The streaming kernel gives each SM whole chunks of rows; with fewer rows
-  // than two per SM a block per row spreads them wider.
-  if (v <= kGradMaxV && M >= 2 * d.sms) {
-    switch (v) {
-      case 1: return launch_quant_grad_stream<1>(src, M, N, lddy, s_w, codes, s_g, counters, n_counters, d, stream);
-      case 2: return launch_quant_grad_stream<2>(src, M, N, lddy, s_w, codes, s_g, counters, n_counters, d, stream);
-      default: return launch_quant_grad_stream<3>(src, M, N, lddy, s_w, codes, s_g, counters, n_counters, d, stream);
-    }
+  // The bulk kernel gives each SM whole rows; with fewer rows than two per SM a
+  // block per row spreads them wider.
+  if (N <= kQuantBulkMaxK && M >= 2 * d.sms) {
+    int gw = 1;
+    while (gw < 4 && gw * kQuantBulkWarpElems < N) gw *= 2;
+    const int64_t room = d.max_smem_optin - 2048;
+    int64_t slots = (room - 4 * N) / (2 * N);
+    if (slots > kGradMaxSlots) slots = kGradMaxSlots;
+    int st = ensure_smem_limit<quant_grad_bulk_kernel>(static_cast<int>(room));
+    if (st != W8A8_OK) return st;
+    return launch_ex(true, quant_grad_bulk_kernel, dim3(d.sms), dim3(kGradBulkWarps * 32),
+                     static_cast<size_t>(4 * N + slots * 2 * N), stream, src, static_cast<int>(M), n32,
+                     lddy, s_w, codes, ldc, s_g, gw, static_cast<int>(slots), counters, n_counters);
   }
+  const int64_t v = cdiv(N / 8, kGradThreads);
   switch (v) {
     case 1: return launch_ex(true, quant_grad_rows_kernel<1>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g, counters, n_counters);
     case 2: return launch_ex(true, quant_grad_rows_kernel<2>, grid, dim3(kGradThreads), 0, stream, src, n32, lddy, s_w, codes, ldc, s_g, counters, n_counters);
