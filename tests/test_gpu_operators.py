@@ -425,6 +425,7 @@ def test_group_norm_gradient_against_differences(silu):
 @pytest.mark.parametrize("shape,groups,dtype,pad", [
     ((1, 130001, 128), 32, torch.bfloat16, 0), ((1, 130001, 128), 32, torch.bfloat16, 16),
     ((3, 20011, 320), 32, torch.float32, 0), ((2, 3001, 4096), 32, torch.float16, 0),
+    ((1, 300007, 128), 32, torch.bfloat16, 0), ((148, 1500, 256), 8, torch.bfloat16, 0),  # several rings
 ])
 def test_group_norm_longer_than_the_ring(shape, groups, dtype, pad):
     Bn, S, C = shape

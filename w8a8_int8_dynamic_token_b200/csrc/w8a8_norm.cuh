@@ -804,13 +804,16 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
         }
         __syncthreads();
         for (int i = top; i >= low; --i) {
-          if (warp == 0 && i + 1 < chunks && i + 1 >= NS) fill(b, i + 1 - NS, slot + 1 == NS ? 0 : slot + 1);
+          if (warp == 0 && i < top && i + 1 >= NS) fill(b, i + 1 - NS, slot + 1 == NS ? 0 : slot + 1);
           codes(norm_smem + slot * slot_bytes + offset, row_max + slot * chunk_rows,
                 i == chunks - 1 ? last_nb : (live ? K : 0),
                 static_cast<int64_t>(b) * p.S + lo + static_cast<int64_t>(i) * chunk_rows + row);
           release(slot);
           slot = slot == 0 ? NS - 1 : slot - 1;
         }
+        // the next window's maxima need all of its chunks, the one that takes
+        // the slot released last among them
+        if (warp == 0 && low >= NS) fill(b, low - NS, slot + 1 == NS ? 0 : slot + 1);
       }
     } else {
       // where this thread's first row of a chunk goes, from the last chunk down
