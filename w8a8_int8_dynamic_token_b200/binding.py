@@ -569,21 +569,33 @@ def input_grad_workspace_size(M: int, N: int, K: int, variant: int = VARIANT_AUT
     return n
 
 
-def _scratch(need, workspace, dev):
+def _on_device(x, others, stream, call, *args):
+    """call(raw stream handle, *args) on x's device and on the given or its
+    current stream (see _launching; nothing is entered where neither has to be
+    switched).  Every tensor of `others` (None allowed) must be on x's device."""
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"a tensor is on {t.device}, expected cuda:{index} (all must be CUDA "
+                             "tensors on one device)")
+    if stream is None and index == torch._C._cuda_getDevice():
+        return call(torch._C._cuda_getCurrentRawStream(index), *args)
+    with _switching(x.device, stream) as s:
+        return call(s.cuda_stream, *args)
+
+
+def _scratch(need, workspace, x):
     """(tensor, pointer, bytes) of the caller's workspace, or of a fresh one of
-    `need` bytes (allocated on the launching stream, inside _launching; kept
-    alive by the caller until the launches have been enqueued)."""
+    `need` bytes on x's device (allocated on the launching stream; kept alive by
+    the caller until the launches have been enqueued)."""
     if workspace is None:
         if need == 0:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
         return workspace, workspace.data_ptr(), need
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _handle(s) -> int:
-    """The raw handle of what _launching yields."""
-    return s if isinstance(s, int) else s.cuda_stream
 
 
 def _address(t):
@@ -604,15 +616,18 @@ def linear_input_grad(dy, Wq, s_w, out=None, workspace=None, variant=VARIANT_AUT
     if out is not None:
         _need(out, "out", torch.bfloat16, 2)
         _shape(out, "out", (M, K))
-    dev = _on_one_device(dy=dy, Wq=Wq, s_w=s_w, out=out, workspace=workspace)
-    need = input_grad_workspace_size(M, N, K, variant)
-    with _launching(dev, stream) as s:
-        dx = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-        ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
-        _check(w8a8_linear_input_grad(dy.data_ptr(), M, N, dy.stride(0), Wq.data_ptr(),
-                                      s_w.data_ptr(), K, dx.data_ptr(), dx.stride(0), variant,
-                                      ws_ptr, ws_bytes, _handle(s)), "w8a8_linear_input_grad")
-        del ws
+    return _on_device(dy, (Wq, s_w, out, workspace), stream, _linear_input_grad, dy, Wq, s_w, M, N, K,
+                      out, workspace, variant, input_grad_workspace_size(M, N, K, variant))
+
+
+def _linear_input_grad(handle, dy, Wq, s_w, M, N, K, out, workspace, variant, need):
+    dx = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, dy)
+    st = w8a8_linear_input_grad(dy.data_ptr(), M, N, dy.stride(0), Wq.data_ptr(), s_w.data_ptr(), K,
+                                dx.data_ptr(), dx.stride(0), variant, ws_ptr, ws_bytes, handle)
+    del ws  # enqueued: later allocations on the stream are ordered after the launches
+    if st != W8A8_OK:
+        raise W8A8Error(st, "w8a8_linear_input_grad")
     return dx
 
 
@@ -734,21 +749,28 @@ def rotary(x, positions, inv_freq, k=None, layout="interleaved", axis=None, scal
         raise TypeError("axis must be a dense CPU int32 tensor of inv_freq's shape")
     pos_b, pos_t, axes = _position_strides(positions.shape, positions.stride(), batch, tokens,
                                            axis is not None)
-    dev = _on_one_device(x=x, k=k, positions=positions, out=out, out_k=out_k)
-    with _launching(dev, stream) as s:
-        y = out if out is not None else torch.empty_like(x)
-        _, (yb, yt, yh) = _head_strides(y.shape, y.stride(), "out")
-        tensors = (RotaryHeads * 2)((x.data_ptr(), y.data_ptr(), heads, xb, xt, xh, yb, yt, yh))
-        y_k = None
-        if k is not None:
-            y_k = out_k if out_k is not None else torch.empty_like(k)
-            _, (yb, yt, yh) = _head_strides(y_k.shape, y_k.stride(), "out_k")
-            tensors[1] = (k.data_ptr(), y_k.data_ptr(), k_heads, kb, kt, kh, yb, yt, yh)
-        _check(w8a8_rotary(tensors, 1 if k is None else 2, _DTYPES[dtype], batch, tokens, dim, rot,
-                           _LAYOUTS[layout], positions.data_ptr(),
-                           64 if positions.dtype == torch.int64 else 32, pos_b, pos_t, axes,
-                           inv_freq.data_ptr(), _address(axis), scale, 1 if backward else 0,
-                           _handle(s)), "w8a8_rotary")
+    return _on_device(x, (k, positions, out, out_k), stream, _rotary, x, k, out, out_k,
+                      (heads, xb, xt, xh), None if k is None else (k_heads, kb, kt, kh), batch,
+                      tokens, dim, rot, _LAYOUTS[layout], positions, pos_b, pos_t, axes, inv_freq,
+                      axis, scale, 1 if backward else 0)
+
+
+def _rotary(handle, x, k, out, out_k, x_heads, k_heads, batch, tokens, dim, rot, layout, positions,
+            pos_b, pos_t, axes, inv_freq, axis, scale, backward):
+    y = out if out is not None else torch.empty_like(x)
+    _, ys = _head_strides(y.shape, y.stride(), "out")
+    tensors = (RotaryHeads * 2)((x.data_ptr(), y.data_ptr(), *x_heads, *ys))
+    y_k = None
+    if k is not None:
+        y_k = out_k if out_k is not None else torch.empty_like(k)
+        _, ys = _head_strides(y_k.shape, y_k.stride(), "out_k")
+        tensors[1] = (k.data_ptr(), y_k.data_ptr(), *k_heads, *ys)
+    st = w8a8_rotary(tensors, 1 if k is None else 2, _DTYPES[x.dtype], batch, tokens, dim, rot,
+                     layout, positions.data_ptr(), 64 if positions.dtype == torch.int64 else 32,
+                     pos_b, pos_t, axes, inv_freq.data_ptr(), _address(axis), scale, backward,
+                     handle)
+    if st != W8A8_OK:
+        raise W8A8Error(st, "w8a8_rotary")
     return y if k is None else (y, y_k)
 
 
@@ -809,6 +831,20 @@ def _activation(activation):
     return _ACTIVATIONS[activation]
 
 
+def _norm_out(x, out):
+    """out, or a dense new tensor like x, and its strides."""
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    return out, _pixels(out.shape, out.stride(), "out")
+
+
+def _norm_stats(wanted, B, groups, x):
+    if not wanted:
+        return None, None
+    return (torch.empty((B, groups), dtype=torch.float32, device=x.device),
+            torch.empty((B, groups), dtype=torch.float32, device=x.device))
+
+
 def group_norm(x, groups, weight=None, bias=None, eps=1e-5, activation=None, out=None,
                return_stats=False, workspace=None, stream=None):
     """Group normalization of a channels-last x [B, ..., C] (bf16, fp16, fp32)
@@ -816,28 +852,30 @@ def group_norm(x, groups, weight=None, bias=None, eps=1e-5, activation=None, out
     mean and 1 / standard deviation, fp32 [B, groups], that the backward pass
     takes).  out may be x itself."""
     _channels_last(x, "x")
-    B, S, C, xb, xs = _pixels(x.shape, x.stride(), "x")
+    geometry = _pixels(x.shape, x.stride(), "x")
     act = _activation(activation)
-    pdt = _norm_params(x, C, weight, bias)
+    pdt = _norm_params(x, geometry[2], weight, bias)
     if out is not None:
         _channels_last(out, "out", x.dtype)
         _shape(out, "out", x.shape)
-    dev = _on_one_device(x=x, weight=weight, bias=bias, out=out, workspace=workspace)
-    need = group_norm_workspace_size(B, S, C, groups, x.dtype)
-    with _launching(dev, stream) as s:
-        y = out
-        if y is None:
-            y = torch.empty_like(x, memory_format=torch.contiguous_format)
-        _, _, _, yb, ys = _pixels(y.shape, y.stride(), "out")
-        mean = rstd = None
-        if return_stats:
-            mean, rstd = torch.empty((2, B, groups), dtype=torch.float32, device=dev).unbind()
-        ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
-        _check(w8a8_group_norm(x.data_ptr(), xb, xs, _DTYPES[x.dtype], B, S, C, groups,
-                               _address(weight), _address(bias), pdt, eps, act, y.data_ptr(), yb,
-                               ys, _address(mean), _address(rstd), ws_ptr, ws_bytes, _handle(s)),
-               "w8a8_group_norm")
-        del ws
+    return _on_device(x, (weight, bias, out, workspace), stream, _group_norm, x, geometry, groups,
+                      weight, bias, pdt, eps, act, out, return_stats, workspace)
+
+
+def _group_norm(handle, x, geometry, groups, weight, bias, pdt, eps, act, out, return_stats,
+                workspace):
+    B, S, C, xb, xs = geometry
+    dtype = x.dtype
+    need = group_norm_workspace_size(B, S, C, groups, dtype)
+    y, (_, _, _, yb, ys) = _norm_out(x, out)
+    mean, rstd = _norm_stats(return_stats, B, groups, x)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, x)
+    st = w8a8_group_norm(x.data_ptr(), xb, xs, _DTYPES[dtype], B, S, C, groups, _address(weight),
+                         _address(bias), pdt, eps, act, y.data_ptr(), yb, ys, _address(mean),
+                         _address(rstd), ws_ptr, ws_bytes, handle)
+    del ws  # enqueued: later allocations on the stream are ordered after the launch
+    if st != W8A8_OK:
+        raise W8A8Error(st, "w8a8_group_norm")
     return (y, mean, rstd) if return_stats else y
 
 
@@ -847,23 +885,27 @@ def group_norm_quant(x, groups, weight=None, bias=None, eps=1e-5, activation=Non
     C], s_a fp32 [B * pixels]), the rows of the fp32 result quantized per pixel
     (and the statistics, with return_stats)."""
     _channels_last(x, "x", torch.bfloat16)
-    B, S, C, xb, xs = _pixels(x.shape, x.stride(), "x")
+    geometry = _pixels(x.shape, x.stride(), "x")
     act = _activation(activation)
-    pdt = _norm_params(x, C, weight, bias)
-    dev = _on_one_device(x=x, weight=weight, bias=bias, workspace=workspace)
+    pdt = _norm_params(x, geometry[2], weight, bias)
+    return _on_device(x, (weight, bias, workspace), stream, _group_norm_quant, x, geometry, groups,
+                      weight, bias, pdt, eps, act, return_stats, workspace)
+
+
+def _group_norm_quant(handle, x, geometry, groups, weight, bias, pdt, eps, act, return_stats,
+                      workspace):
+    B, S, C, xb, xs = geometry
     need = group_norm_workspace_size(B, S, C, groups, x.dtype)
-    with _launching(dev, stream) as s:
-        q = torch.empty((B * S, C), dtype=torch.int8, device=dev)
-        s_a = torch.empty(B * S, dtype=torch.float32, device=dev)
-        mean = rstd = None
-        if return_stats:
-            mean, rstd = torch.empty((2, B, groups), dtype=torch.float32, device=dev).unbind()
-        ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
-        _check(w8a8_group_norm_quant(x.data_ptr(), xb, xs, B, S, C, groups, _address(weight),
-                                     _address(bias), pdt, eps, act, q.data_ptr(), s_a.data_ptr(),
-                                     _address(mean), _address(rstd), ws_ptr, ws_bytes, _handle(s)),
-               "w8a8_group_norm_quant")
-        del ws
+    q = torch.empty((B * S, C), dtype=torch.int8, device=x.device)
+    s_a = torch.empty(B * S, dtype=torch.float32, device=x.device)
+    mean, rstd = _norm_stats(return_stats, B, groups, x)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, x)
+    st = w8a8_group_norm_quant(x.data_ptr(), xb, xs, B, S, C, groups, _address(weight),
+                               _address(bias), pdt, eps, act, q.data_ptr(), s_a.data_ptr(),
+                               _address(mean), _address(rstd), ws_ptr, ws_bytes, handle)
+    del ws
+    if st != W8A8_OK:
+        raise W8A8Error(st, "w8a8_group_norm_quant")
     return (q, s_a, mean, rstd) if return_stats else (q, s_a)
 
 
@@ -874,39 +916,47 @@ def group_norm_backward(dy, x, mean, rstd, weight=None, bias=None, activation=No
     there is no such parameter).  mean, rstd: the forward's statistics; out may
     be dy or x itself."""
     _channels_last(x, "x")
-    B, S, C, xb, xs = _pixels(x.shape, x.stride(), "x")
+    geometry = _pixels(x.shape, x.stride(), "x")
     _channels_last(dy, "dy", x.dtype)
     _shape(dy, "dy", x.shape)
-    _, _, _, gb, gs = _pixels(dy.shape, dy.stride(), "dy")
     act = _activation(activation)
-    pdt = _norm_params(x, C, weight, bias)
+    pdt = _norm_params(x, geometry[2], weight, bias)
     _need(mean, "mean", torch.float32, 2)
-    groups = mean.shape[1]
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _need(t, name, torch.float32, 2)
-        _shape(t, name, (B, groups))
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be dense")
+    _need(rstd, "rstd", torch.float32, 2)
+    B, groups = mean.shape
+    if B != geometry[0]:
+        raise ValueError(f"mean must have shape ({geometry[0]}, groups), got {tuple(mean.shape)}")
+    _shape(rstd, "rstd", mean.shape)
+    if not (mean.is_contiguous() and rstd.is_contiguous()):
+        raise ValueError("mean and rstd must be dense")
     if out is not None:
         _channels_last(out, "out", x.dtype)
         _shape(out, "out", x.shape)
-    dev = _on_one_device(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, bias=bias, out=out,
-                         workspace=workspace)
-    need = group_norm_workspace_size(B, S, C, groups, x.dtype, True)
-    with _launching(dev, stream) as s:
-        dx = out
-        if dx is None:
-            dx = torch.empty_like(x, memory_format=torch.contiguous_format)
-        _, _, _, ob, os_ = _pixels(dx.shape, dx.stride(), "out")
-        dweight = None if weight is None else torch.empty(C, dtype=torch.float32, device=dev)
-        dbias = None if bias is None else torch.empty(C, dtype=torch.float32, device=dev)
-        ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
-        _check(w8a8_group_norm_backward(dy.data_ptr(), gb, gs, x.data_ptr(), xb, xs,
-                                        _DTYPES[x.dtype], B, S, C, groups, mean.data_ptr(),
-                                        rstd.data_ptr(), _address(weight), _address(bias), pdt, act,
-                                        dx.data_ptr(), ob, os_, _address(dweight), _address(dbias),
-                                        ws_ptr, ws_bytes, _handle(s)), "w8a8_group_norm_backward")
-        del ws
+    return _on_device(x, (dy, mean, rstd, weight, bias, out, workspace), stream,
+                      _group_norm_backward, dy, x, geometry, groups, mean, rstd, weight, bias, pdt,
+                      act, out, workspace)
+
+
+def _group_norm_backward(handle, dy, x, geometry, groups, mean, rstd, weight, bias, pdt, act, out,
+                         workspace):
+    B, S, C, xb, xs = geometry
+    dtype = x.dtype
+    _, _, _, gb, gs = _pixels(dy.shape, dy.stride(), "dy")
+    need = group_norm_workspace_size(B, S, C, groups, dtype, True)
+    dx, (_, _, _, ob, os_) = _norm_out(x, out)
+    dweight = dbias = None
+    if weight is not None:
+        dweight = torch.empty(C, dtype=torch.float32, device=x.device)
+    if bias is not None:
+        dbias = torch.empty(C, dtype=torch.float32, device=x.device)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, x)
+    st = w8a8_group_norm_backward(dy.data_ptr(), gb, gs, x.data_ptr(), xb, xs, _DTYPES[dtype], B, S,
+                                  C, groups, mean.data_ptr(), rstd.data_ptr(), _address(weight),
+                                  _address(bias), pdt, act, dx.data_ptr(), ob, os_,
+                                  _address(dweight), _address(dbias), ws_ptr, ws_bytes, handle)
+    del ws
+    if st != W8A8_OK:
+        raise W8A8Error(st, "w8a8_group_norm_backward")
     return dx, dweight, dbias
 
 
