@@ -359,7 +359,8 @@ typedef struct {
  * radians per position (finite, >= 0), any scaling for long contexts applied;
  * axis: HOST array of rot / 2 axis indices, or NULL (all 0).  Both are read
  * before the call returns.
- * y is x itself with the same strides, or does not overlap it.  dim and rot
+ * y is x itself with the same strides, or does not overlap it (nor another
+ * tensor of the call).  dim and rot
  * even, rot <= dim <= 512, batch * tokens < 2^30.  Accesses are 16 bytes wide
  * where pointers, strides, dim and rot allow, else single values.
  */
@@ -392,11 +393,17 @@ typedef enum { W8A8_ACT_NONE = 0, W8A8_ACT_SILU = 1 } w8a8_activation;
  * with xh = (x - mean) * rstd and E over the group; dx in x's type, which may
  * be dy or x itself with the same strides.  Sums run in a fixed order: equal
  * inputs give equal bits.
- * C % 8 == 0, C <= 4096 (2048 in fp32), strides multiples of 8 and at least
- * C where their extent is above 1, B * S < 2^30, x, dy, y, q, weight, bias
+ * C % 8 == 0, C <= 4096 (2048 in fp32), strides of extents above 1 multiples
+ * of 8 and at least C, B * S < 2^30, x, dy, y, q, weight, bias
  * 16-byte aligned.
- * workspace: w8a8_group_norm_workspace_size bytes, 16-byte aligned, no
- * initialization needed.
+ * workspace: w8a8_group_norm_workspace_size bytes (0 for a forward form whose
+ * samples take one block each), 16-byte aligned, no initialization needed; it must not be in
+ * use by other work while the call runs.  One launch (the gradient of
+ * parameters: two).  The blocks of a sample wait for one another, so they are
+ * launched cooperatively and all run at once; every wait is bounded (see
+ * w8a8_last_device_error), and after a launch that reported
+ * W8A8_ERR_DEVICE_TIMEOUT, replaying a captured graph of it on the same
+ * workspace is outside the contract.
  */
 W8A8_API int w8a8_group_norm_workspace_size(int64_t B, int64_t S, int64_t C, int64_t G, int dtype,
                                             int backward, size_t *bytes);

@@ -343,6 +343,31 @@ def test_group_norm_quant_zero_rows():
     assert (q == 0).all() and (s == 0).all()
 
 
+@pytest.mark.parametrize("size", [6e37, 2e37, 5e36, 1e-29, 1e-32])
+def test_group_norm_quant_rows_at_the_ends_of_fp32(size):
+    # weights that put a row's maximum near fp32's largest or smallest values
+    x = make_norm((1, 20, 32), torch.bfloat16, "none", 0.0)[0]
+    w = torch.full((32,), size)
+    q, s, mean, rstd = w8a8.group_norm_quant(x.cuda(), 4, w.cuda(), return_stats=True)
+    y64, m64, r64, z64, xh64 = norm64(x, 4, w, None, 1e-5, False)
+    slack = norm_slack(x, y64, m64, r64, z64, xh64, w, None, False)[0]
+    y64 = y64[0]
+    amax = y64.abs().amax(1)
+    close(s, amax / 127, slack.amax(1) / 127 + 2 * U * amax / 127, "scales")
+    s64 = s.cpu().double()[:, None]
+    # half a code, and what the quotient's rounding moves
+    assert ((q.cpu().double() * s64 - y64).abs() <= s64 * (0.5 + 127 * 2 * U) + slack).all()
+
+
+def test_group_norm_extents_of_one_have_no_stride():
+    x = torch.randn((1, 9, 16), generator=gen(13)).bfloat16().cuda()
+    want = w8a8.group_norm(x, 2)
+    odd = torch.as_strided(x, (1, 9, 16), (149, 16, 1))
+    assert torch.equal(w8a8.group_norm(odd, 2, out=torch.as_strided(torch.empty_like(x), (1, 9, 16), (3, 16, 1))), want)
+    one = torch.as_strided(x, (9, 1, 16), (16, 5, 1))
+    assert torch.equal(w8a8.group_norm(one, 2), w8a8.group_norm(x.view(9, 1, 16).contiguous(), 2))
+
+
 def grads64(dy, x, G, w, b, mean, rstd, silu):
     Bn, S, C = x.shape
     sh = (Bn, S, G, C // G)

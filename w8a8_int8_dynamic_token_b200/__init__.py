@@ -3,8 +3,10 @@
 The layer: per-token symmetric int8 quantization of bf16 activations, an
 int8 x int8 -> int32 GEMM against per-output-channel int8 weights on the
 tcgen05 tensor cores (or a streaming GEMV for M <= 16), and a fused fp32
-dequantization/bias epilogue producing bf16.  The kernels live in
-``libw8a8.so`` (C ABI: ``include/w8a8.h``); this package is its binding.
+dequantization/bias epilogue producing bf16.  Beside it, what stands around the
+layer in a transformer block: rotary positions on the heads it wrote, group norm
+(also straight to the layer's int8 rows), and the gradients of all three (the
+layer's with respect to its input).  The kernels live in ``libw8a8.so`` (C ABI: ``include/w8a8.h``); this package is its binding.
 """
 from .binding import (  # noqa: F401
     LIB_PATH, VARIANT_AUTO, VARIANT_GEMM_BN64, VARIANT_GEMM_BN128, VARIANT_GEMM_BN256,

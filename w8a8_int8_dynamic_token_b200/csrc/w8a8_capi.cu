@@ -1215,10 +1215,11 @@ int check_norm(int64_t B, int64_t S, int64_t C, int64_t G, int dtype) {
   return W8A8_OK;
 }
 
-// Strides of a sample and a pixel: whole rows, 16-byte steps.
+// Strides of a sample and a pixel: whole rows, 16-byte steps (an extent of one
+// has no stride).
 int check_norm_strides(int64_t B, int64_t S, int64_t C, int64_t sb, int64_t ss) {
   if ((S > 1 && ss < C) || (B > 1 && sb < C)) return W8A8_ERR_INVALID_ARG;
-  if (sb % 8 != 0 || ss % 8 != 0) return W8A8_ERR_UNSUPPORTED_SHAPE;
+  if ((B > 1 && sb % 8 != 0) || (S > 1 && ss % 8 != 0)) return W8A8_ERR_UNSUPPORTED_SHAPE;
   return W8A8_OK;
 }
 
@@ -1513,7 +1514,7 @@ const char *w8a8_status_string(int status) {
   }
 }
 
-const char *w8a8_version(void) { return "w8a8 1.1 sm_100a"; }
+const char *w8a8_version(void) { return "w8a8 1.2 sm_100a"; }
 
 int w8a8_bench_mma_i8_peak(int64_t iterations, int32_t pairs, w8a8_stream_t stream) {
   if (iterations < 1 || iterations > 500000 || pairs < 1) return W8A8_ERR_INVALID_ARG;

@@ -763,10 +763,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
             // rint(y * (127 / amax)) in one fused step: y is a rounded fp32
             // value already, so a quotient off by 2^-22 moves a code only
             // where y is that close to a tie; the scale is the IEEE quotient.
-            // Next to the subnormals, where 127 / amax leaves fp32, divide.
+            // Next to the subnormals, where 127 / amax leaves fp32, and beyond
+            // 2^126, where the fast quotient is 0, divide.
             const float amax = __uint_as_float(mx[row + k * p.rpi]);
             uint32_t code[V];
-            if (amax >= 1e-30f) {
+            if (amax >= 1e-30f && amax <= 1e37f) {
               const float r = __fdividef(127.0f, amax);
 #pragma unroll
               for (int h = 0; h < H; ++h) {
