@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kGradThreads)
 }
 
 // The same rows for many of them: one block of 16 warps per SM, persistent, in
-// groups of G warps (1, 2 or 4: at most 3072 columns per warp), each on a row
+// groups of G warps (1, 2 or 4, as in quant_rows_bulk_kernel), each on a row
 // of its own, so that the groups' phases fill one another's latencies.  The
 // channel scales lie in shared memory, as two arrays of the even and odd
 // 16-byte halves of a vector's eight (32-byte steps between lanes would
