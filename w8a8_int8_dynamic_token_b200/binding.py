@@ -18,6 +18,7 @@ import functools
 import math
 import os
 import re
+import struct
 
 import torch
 
@@ -78,6 +79,10 @@ class RotaryHeads(ctypes.Structure):
                 ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64)]
 
 
+# The arrays of RotaryHeads of a call, packed (as bytes: a third of the time of
+# filling the structures).
+_ONE_HEADS, _TWO_HEADS = struct.Struct("9q").pack, struct.Struct("18q").pack
+
 _lib = None
 _vp, _i64, _i32, _int, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int,
                               ctypes.c_size_t)
@@ -107,7 +112,7 @@ _SIGNATURES = {
     "w8a8_input_grad_workspace_size": ([_i64, _i64, _i64, _int, ctypes.POINTER(_sz)], _int),
     "w8a8_linear_input_grad": ([_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _int, _vp, _sz,
                                 _vp], _int),
-    "w8a8_rotary": ([ctypes.POINTER(RotaryHeads), _int, _int, _i64, _i64, _i64, _i64, _int, _vp,
+    "w8a8_rotary": ([_vp, _int, _int, _i64, _i64, _i64, _i64, _int, _vp,
                      _int, _i64, _i64, _i64, _vp, _vp, _f32, _int, _vp], _int),
     "w8a8_group_norm_workspace_size": ([_i64, _i64, _i64, _i64, _int, _int, ctypes.POINTER(_sz)],
                                        _int),
@@ -569,10 +574,10 @@ def input_grad_workspace_size(M: int, N: int, K: int, variant: int = VARIANT_AUT
     return n
 
 
-def _on_device(x, others, stream, call, *args):
-    """call(raw stream handle, *args) on x's device and on the given or its
-    current stream (see _launching; nothing is entered where neither has to be
-    switched).  Every tensor of `others` (None allowed) must be on x's device."""
+def _launch_handle(x, others, stream):
+    """The raw handle of the stream a call on x's device goes to, or None where
+    the device or the stream has to be switched first (see _launching).  Every
+    tensor of `others` (None allowed) must be on x's device."""
     index = x.get_device()
     if index < 0:
         raise ValueError("the tensors must be CUDA tensors")
@@ -581,9 +586,8 @@ def _on_device(x, others, stream, call, *args):
             raise ValueError(f"a tensor is on {t.device}, expected cuda:{index} (all must be CUDA "
                              "tensors on one device)")
     if stream is None and index == torch._C._cuda_getDevice():
-        return call(torch._C._cuda_getCurrentRawStream(index), *args)
-    with _switching(x.device, stream) as s:
-        return call(s.cuda_stream, *args)
+        return torch._C._cuda_getCurrentRawStream(index)
+    return None
 
 
 def _scratch(need, workspace, x):
@@ -616,15 +620,17 @@ def linear_input_grad(dy, Wq, s_w, out=None, workspace=None, variant=VARIANT_AUT
     if out is not None:
         _need(out, "out", torch.bfloat16, 2)
         _shape(out, "out", (M, K))
-    return _on_device(dy, (Wq, s_w, out, workspace), stream, _linear_input_grad, dy, Wq, s_w, M, N, K,
-                      out, workspace, variant, input_grad_workspace_size(M, N, K, variant))
-
-
-def _linear_input_grad(handle, dy, Wq, s_w, M, N, K, out, workspace, variant, need):
-    dx = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
+    need = input_grad_workspace_size(M, N, K, variant)
+    handle = _launch_handle(dy, (Wq, s_w, out, workspace), stream)
+    if handle is None:
+        with _switching(dy.device, stream):
+            return linear_input_grad(dy, Wq, s_w, out, workspace, variant)
+    dx = out if out is not None else torch.empty_strided((M, K), (K, 1), dtype=torch.bfloat16,
+                                                         device=dy.device)
     ws, ws_ptr, ws_bytes = _scratch(need, workspace, dy)
-    st = w8a8_linear_input_grad(dy.data_ptr(), M, N, dy.stride(0), Wq.data_ptr(), s_w.data_ptr(), K,
-                                dx.data_ptr(), dx.stride(0), variant, ws_ptr, ws_bytes, handle)
+    st = lib().w8a8_linear_input_grad(dy.data_ptr(), M, N, dy.stride(0), Wq.data_ptr(),
+                                      s_w.data_ptr(), K, dx.data_ptr(), dx.stride(0), variant,
+                                      ws_ptr, ws_bytes, handle)
     del ws  # enqueued: later allocations on the stream are ordered after the launches
     if st != W8A8_OK:
         raise W8A8Error(st, "w8a8_linear_input_grad")
@@ -692,7 +698,6 @@ def _head_strides(shape, strides, name):
     return (shape[0] if four else 1, *shape[-3:]), (strides[0] if four else 0, *strides[-3:-1])
 
 
-@functools.lru_cache(maxsize=4096)
 def _position_strides(shape, strides, batch, tokens, with_axes):
     """(batch stride, token stride, axes) of positions."""
     lead = len(shape) - with_axes
@@ -703,6 +708,26 @@ def _position_strides(shape, strides, batch, tokens, with_axes):
     if axes > 1 and strides[-1] != 1:
         raise ValueError("positions must have unit stride in its last dimension")
     return strides[0] if lead == 2 else 0, strides[lead - 1], axes
+
+
+@functools.lru_cache(maxsize=4096)
+def _rotary_geometry(x_shape, x_strides, k_shape, k_strides, pos_shape, pos_strides, pairs, layout,
+                     with_axes):
+    """What a call's shapes and strides say, checked once: ((heads, strides) of
+    x, of k or None, sizes and codes up to the layout, strides of positions)."""
+    (batch, tokens, heads, dim), xs = _head_strides(x_shape, x_strides, "x")
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+    if 2 * pairs > dim:
+        raise ValueError(f"inv_freq turns {2 * pairs} values of a head, which has {dim}")
+    k = None
+    if k_shape is not None:
+        (k_batch, k_tokens, k_heads, k_dim), ks = _head_strides(k_shape, k_strides, "k")
+        if len(k_shape) != len(x_shape) or (k_batch, k_tokens, k_dim) != (batch, tokens, dim):
+            raise ValueError("x and k differ in more than their heads")
+        k = (k_heads, *ks)
+    return ((heads, *xs), k, (batch, tokens, dim, 2 * pairs, _LAYOUTS[layout]),
+            _position_strides(pos_shape, pos_strides, batch, tokens, with_axes))
 
 
 def rotary(x, positions, inv_freq, k=None, layout="interleaved", axis=None, scale=1.0,
@@ -719,56 +744,46 @@ def rotary(x, positions, inv_freq, k=None, layout="interleaved", axis=None, scal
     where those are dense."""
     _heads(x, "x", None)
     dtype = x.dtype
-    (batch, tokens, heads, dim), (xb, xt, xh) = _head_strides(x.shape, x.stride(), "x")
-    if layout not in _LAYOUTS:
-        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or \
             inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a dense 1-D CPU float64 tensor")
-    rot = 2 * inv_freq.shape[0]
-    if rot > dim:
-        raise ValueError(f"inv_freq turns {rot} values of a head, which has {dim}")
-    if out is not None:
-        _heads(out, "out", dtype)
-        _shape(out, "out", x.shape)
     if k is not None:
         _heads(k, "k", dtype)
-        (kb_, kt_, k_heads, kd_), (kb, kt, kh) = _head_strides(k.shape, k.stride(), "k")
-        if k.dim() != x.dim() or (kb_, kt_, kd_) != (batch, tokens, dim):
-            raise ValueError("x and k differ in more than their heads")
-        if out_k is not None:
-            _heads(out_k, "out_k", dtype)
-            _shape(out_k, "out_k", k.shape)
-    elif out_k is not None:
-        raise ValueError("out_k is given without k")
     if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
         raise TypeError("positions must be an int32 or int64 tensor")
     if axis is not None and (
             not isinstance(axis, torch.Tensor) or axis.dtype != torch.int32 or axis.is_cuda or
             axis.shape != inv_freq.shape or not axis.is_contiguous()):
         raise TypeError("axis must be a dense CPU int32 tensor of inv_freq's shape")
-    pos_b, pos_t, axes = _position_strides(positions.shape, positions.stride(), batch, tokens,
-                                           axis is not None)
-    return _on_device(x, (k, positions, out, out_k), stream, _rotary, x, k, out, out_k,
-                      (heads, xb, xt, xh), None if k is None else (k_heads, kb, kt, kh), batch,
-                      tokens, dim, rot, _LAYOUTS[layout], positions, pos_b, pos_t, axes, inv_freq,
-                      axis, scale, 1 if backward else 0)
-
-
-def _rotary(handle, x, k, out, out_k, x_heads, k_heads, batch, tokens, dim, rot, layout, positions,
-            pos_b, pos_t, axes, inv_freq, axis, scale, backward):
+    geometry = _rotary_geometry(
+        x.shape, x.stride(), None if k is None else k.shape, None if k is None else k.stride(),
+        positions.shape, positions.stride(), inv_freq.shape[0], layout, axis is not None)
+    if out is not None:
+        _heads(out, "out", dtype)
+        _shape(out, "out", x.shape)
+    if out_k is not None:
+        if k is None:
+            raise ValueError("out_k is given without k")
+        _heads(out_k, "out_k", dtype)
+        _shape(out_k, "out_k", k.shape)
+    handle = _launch_handle(x, (k, positions, out, out_k), stream)
+    if handle is None:
+        with _switching(x.device, stream):
+            return rotary(x, positions, inv_freq, k, layout, axis, scale, backward, out, out_k)
+    x_heads, k_heads, sizes, pos = geometry
     y = out if out is not None else torch.empty_like(x)
-    _, ys = _head_strides(y.shape, y.stride(), "out")
-    tensors = (RotaryHeads * 2)((x.data_ptr(), y.data_ptr(), *x_heads, *ys))
+    ys = _head_strides(y.shape, y.stride(), "out")[1]
     y_k = None
-    if k is not None:
+    if k is None:
+        tensors = _ONE_HEADS(x.data_ptr(), y.data_ptr(), *x_heads, *ys)
+    else:
         y_k = out_k if out_k is not None else torch.empty_like(k)
-        _, ys = _head_strides(y_k.shape, y_k.stride(), "out_k")
-        tensors[1] = (k.data_ptr(), y_k.data_ptr(), *k_heads, *ys)
-    st = w8a8_rotary(tensors, 1 if k is None else 2, _DTYPES[x.dtype], batch, tokens, dim, rot,
-                     layout, positions.data_ptr(), 64 if positions.dtype == torch.int64 else 32,
-                     pos_b, pos_t, axes, inv_freq.data_ptr(), _address(axis), scale, backward,
-                     handle)
+        ks = _head_strides(y_k.shape, y_k.stride(), "out_k")[1]
+        tensors = _TWO_HEADS(x.data_ptr(), y.data_ptr(), *x_heads, *ys, k.data_ptr(),
+                             y_k.data_ptr(), *k_heads, *ks)
+    st = lib().w8a8_rotary(tensors, 1 if k is None else 2, _DTYPES[dtype], *sizes,
+                           positions.data_ptr(), 64 if positions.dtype == torch.int64 else 32, *pos,
+                           inv_freq.data_ptr(), _address(axis), scale, 1 if backward else 0, handle)
     if st != W8A8_OK:
         raise W8A8Error(st, "w8a8_rotary")
     return y if k is None else (y, y_k)
@@ -787,6 +802,7 @@ def _channels_last(t, name, dtype=None):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
+    return t.dtype
 
 
 @functools.lru_cache(maxsize=4096)
@@ -809,20 +825,28 @@ def _pixels(sizes, strides, name):
     return sizes[0], pixels, sizes[-1], strides[0], step
 
 
-def _norm_params(x, C, weight, bias):
+@functools.lru_cache(maxsize=4096)
+def _norm_geometry(sizes, strides, groups, dtype, backward):
+    """_pixels of x and the bytes of workspace that a call takes."""
+    B, S, C, xb, xs = _pixels(sizes, strides, "x")
+    return B, S, C, xb, xs, group_norm_workspace_size(B, S, C, groups, dtype, backward)
+
+
+def _norm_params(dtype, C, weight, bias):
     """The type code of weight and bias ([C], both in x's type or in fp32)."""
-    dtype = x.dtype
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or (t.dtype != x.dtype and t.dtype != torch.float32):
-            raise TypeError(f"{name} must be a {x.dtype} or float32 tensor")
-        if t.shape != (C,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a dense [{C}] tensor")
-        dtype = t.dtype
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+    wt = dtype if weight is None else _norm_param(dtype, C, "weight", weight)
+    bt = wt if bias is None else _norm_param(dtype, C, "bias", bias)
+    if weight is not None and bt is not wt:
         raise TypeError("weight and bias must have the same type")
-    return _DTYPES[dtype]
+    return _DTYPES[bt]
+
+
+def _norm_param(dtype, C, name, t):
+    if not isinstance(t, torch.Tensor) or (t.dtype != dtype and t.dtype != torch.float32):
+        raise TypeError(f"{name} must be a {dtype} or float32 tensor")
+    if t.shape != (C,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a dense [{C}] tensor")
+    return t.dtype
 
 
 def _activation(activation):
@@ -831,18 +855,18 @@ def _activation(activation):
     return _ACTIVATIONS[activation]
 
 
-def _norm_out(x, out):
-    """out, or a dense new tensor like x, and its strides."""
+def _norm_out(x, out, S, C):
+    """out, or a dense new tensor like x, and its strides of a sample and a pixel."""
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    return out, _pixels(out.shape, out.stride(), "out")
+        return torch.empty_like(x, memory_format=torch.contiguous_format), S * C, C
+    return (out, *_pixels(out.shape, out.stride(), "out")[3:])
 
 
 def _norm_stats(wanted, B, groups, x):
     if not wanted:
         return None, None
-    return (torch.empty((B, groups), dtype=torch.float32, device=x.device),
-            torch.empty((B, groups), dtype=torch.float32, device=x.device))
+    mean = torch.empty_strided((B, groups), (groups, 1), dtype=torch.float32, device=x.device)
+    return mean, torch.empty_like(mean)
 
 
 def group_norm(x, groups, weight=None, bias=None, eps=1e-5, activation=None, out=None,
@@ -851,28 +875,23 @@ def group_norm(x, groups, weight=None, bias=None, eps=1e-5, activation=None, out
     with an optional SiLU: y in x's type and shape (and, with return_stats, the
     mean and 1 / standard deviation, fp32 [B, groups], that the backward pass
     takes).  out may be x itself."""
-    _channels_last(x, "x")
-    geometry = _pixels(x.shape, x.stride(), "x")
+    dtype = _channels_last(x, "x")
+    B, S, C, xb, xs, need = _norm_geometry(x.shape, x.stride(), groups, dtype, False)
     act = _activation(activation)
-    pdt = _norm_params(x, geometry[2], weight, bias)
+    pdt = _norm_params(dtype, C, weight, bias)
     if out is not None:
-        _channels_last(out, "out", x.dtype)
+        _channels_last(out, "out", dtype)
         _shape(out, "out", x.shape)
-    return _on_device(x, (weight, bias, out, workspace), stream, _group_norm, x, geometry, groups,
-                      weight, bias, pdt, eps, act, out, return_stats, workspace)
-
-
-def _group_norm(handle, x, geometry, groups, weight, bias, pdt, eps, act, out, return_stats,
-                workspace):
-    B, S, C, xb, xs = geometry
-    dtype = x.dtype
-    need = group_norm_workspace_size(B, S, C, groups, dtype)
-    y, (_, _, _, yb, ys) = _norm_out(x, out)
+    handle = _launch_handle(x, (weight, bias, out, workspace), stream)
+    if handle is None:
+        with _switching(x.device, stream):
+            return group_norm(x, groups, weight, bias, eps, activation, out, return_stats, workspace)
+    y, yb, ys = _norm_out(x, out, S, C)
     mean, rstd = _norm_stats(return_stats, B, groups, x)
     ws, ws_ptr, ws_bytes = _scratch(need, workspace, x)
-    st = w8a8_group_norm(x.data_ptr(), xb, xs, _DTYPES[dtype], B, S, C, groups, _address(weight),
-                         _address(bias), pdt, eps, act, y.data_ptr(), yb, ys, _address(mean),
-                         _address(rstd), ws_ptr, ws_bytes, handle)
+    st = lib().w8a8_group_norm(x.data_ptr(), xb, xs, _DTYPES[dtype], B, S, C, groups,
+                               _address(weight), _address(bias), pdt, eps, act, y.data_ptr(), yb,
+                               ys, _address(mean), _address(rstd), ws_ptr, ws_bytes, handle)
     del ws  # enqueued: later allocations on the stream are ordered after the launch
     if st != W8A8_OK:
         raise W8A8Error(st, "w8a8_group_norm")
@@ -884,25 +903,22 @@ def group_norm_quant(x, groups, weight=None, bias=None, eps=1e-5, activation=Non
     """group_norm of a bf16 x as the operand of linear(): (q int8 [B * pixels,
     C], s_a fp32 [B * pixels]), the rows of the fp32 result quantized per pixel
     (and the statistics, with return_stats)."""
-    _channels_last(x, "x", torch.bfloat16)
-    geometry = _pixels(x.shape, x.stride(), "x")
+    dtype = _channels_last(x, "x", torch.bfloat16)
+    B, S, C, xb, xs, need = _norm_geometry(x.shape, x.stride(), groups, dtype, False)
     act = _activation(activation)
-    pdt = _norm_params(x, geometry[2], weight, bias)
-    return _on_device(x, (weight, bias, workspace), stream, _group_norm_quant, x, geometry, groups,
-                      weight, bias, pdt, eps, act, return_stats, workspace)
-
-
-def _group_norm_quant(handle, x, geometry, groups, weight, bias, pdt, eps, act, return_stats,
-                      workspace):
-    B, S, C, xb, xs = geometry
-    need = group_norm_workspace_size(B, S, C, groups, x.dtype)
-    q = torch.empty((B * S, C), dtype=torch.int8, device=x.device)
+    pdt = _norm_params(dtype, C, weight, bias)
+    handle = _launch_handle(x, (weight, bias, workspace), stream)
+    if handle is None:
+        with _switching(x.device, stream):
+            return group_norm_quant(x, groups, weight, bias, eps, activation, return_stats,
+                                    workspace)
+    q = torch.empty_strided((B * S, C), (C, 1), dtype=torch.int8, device=x.device)
     s_a = torch.empty(B * S, dtype=torch.float32, device=x.device)
     mean, rstd = _norm_stats(return_stats, B, groups, x)
     ws, ws_ptr, ws_bytes = _scratch(need, workspace, x)
-    st = w8a8_group_norm_quant(x.data_ptr(), xb, xs, B, S, C, groups, _address(weight),
-                               _address(bias), pdt, eps, act, q.data_ptr(), s_a.data_ptr(),
-                               _address(mean), _address(rstd), ws_ptr, ws_bytes, handle)
+    st = lib().w8a8_group_norm_quant(x.data_ptr(), xb, xs, B, S, C, groups, _address(weight),
+                                     _address(bias), pdt, eps, act, q.data_ptr(), s_a.data_ptr(),
+                                     _address(mean), _address(rstd), ws_ptr, ws_bytes, handle)
     del ws
     if st != W8A8_OK:
         raise W8A8Error(st, "w8a8_group_norm_quant")
@@ -915,45 +931,39 @@ def group_norm_backward(dy, x, mean, rstd, weight=None, bias=None, activation=No
     group_norm_quant): (dx in x's type, dweight, dbias fp32 [C], None where
     there is no such parameter).  mean, rstd: the forward's statistics; out may
     be dy or x itself."""
-    _channels_last(x, "x")
-    geometry = _pixels(x.shape, x.stride(), "x")
-    _channels_last(dy, "dy", x.dtype)
+    dtype = _channels_last(x, "x")
+    _channels_last(dy, "dy", dtype)
     _shape(dy, "dy", x.shape)
     act = _activation(activation)
-    pdt = _norm_params(x, geometry[2], weight, bias)
     _need(mean, "mean", torch.float32, 2)
     _need(rstd, "rstd", torch.float32, 2)
-    B, groups = mean.shape
-    if B != geometry[0]:
-        raise ValueError(f"mean must have shape ({geometry[0]}, groups), got {tuple(mean.shape)}")
+    groups = mean.shape[1]
+    B, S, C, xb, xs, need = _norm_geometry(x.shape, x.stride(), groups, dtype, True)
+    pdt = _norm_params(dtype, C, weight, bias)
+    if mean.shape[0] != B:
+        raise ValueError(f"mean must have shape ({B}, groups), got {tuple(mean.shape)}")
     _shape(rstd, "rstd", mean.shape)
     if not (mean.is_contiguous() and rstd.is_contiguous()):
         raise ValueError("mean and rstd must be dense")
     if out is not None:
-        _channels_last(out, "out", x.dtype)
+        _channels_last(out, "out", dtype)
         _shape(out, "out", x.shape)
-    return _on_device(x, (dy, mean, rstd, weight, bias, out, workspace), stream,
-                      _group_norm_backward, dy, x, geometry, groups, mean, rstd, weight, bias, pdt,
-                      act, out, workspace)
-
-
-def _group_norm_backward(handle, dy, x, geometry, groups, mean, rstd, weight, bias, pdt, act, out,
-                         workspace):
-    B, S, C, xb, xs = geometry
-    dtype = x.dtype
+    handle = _launch_handle(x, (dy, mean, rstd, weight, bias, out, workspace), stream)
+    if handle is None:
+        with _switching(x.device, stream):
+            return group_norm_backward(dy, x, mean, rstd, weight, bias, activation, out, workspace)
     _, _, _, gb, gs = _pixels(dy.shape, dy.stride(), "dy")
-    need = group_norm_workspace_size(B, S, C, groups, dtype, True)
-    dx, (_, _, _, ob, os_) = _norm_out(x, out)
+    dx, ob, os_ = _norm_out(x, out, S, C)
     dweight = dbias = None
     if weight is not None:
         dweight = torch.empty(C, dtype=torch.float32, device=x.device)
     if bias is not None:
         dbias = torch.empty(C, dtype=torch.float32, device=x.device)
     ws, ws_ptr, ws_bytes = _scratch(need, workspace, x)
-    st = w8a8_group_norm_backward(dy.data_ptr(), gb, gs, x.data_ptr(), xb, xs, _DTYPES[dtype], B, S,
-                                  C, groups, mean.data_ptr(), rstd.data_ptr(), _address(weight),
-                                  _address(bias), pdt, act, dx.data_ptr(), ob, os_,
-                                  _address(dweight), _address(dbias), ws_ptr, ws_bytes, handle)
+    st = lib().w8a8_group_norm_backward(
+        dy.data_ptr(), gb, gs, x.data_ptr(), xb, xs, _DTYPES[dtype], B, S, C, groups,
+        mean.data_ptr(), rstd.data_ptr(), _address(weight), _address(bias), pdt, act, dx.data_ptr(),
+        ob, os_, _address(dweight), _address(dbias), ws_ptr, ws_bytes, handle)
     del ws
     if st != W8A8_OK:
         raise W8A8Error(st, "w8a8_group_norm_backward")
