@@ -711,26 +711,35 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     };
     if constexpr (MODE == kNormQuant) {
       // int8 rows.  Windows of up to a ring of chunks: first every row's
-      // maximum, then, behind one barrier, the codes (y is formed twice: a
-      // barrier per chunk, with y kept, took 10 us where this takes 6, at 2 x
-      // 4096 x 1280).
+      // maximum, then the scales, then the codes, with a barrier between (y is
+      // formed twice: a barrier per chunk, with y kept, took 10 us where this
+      // takes 6, at 2 x 4096 x 1280).  Rows of a chunk without branches between
+      // them and one thread per row for its scale: 262144 x 512 takes 167 us
+      // (202 with each thread dividing for its rows, and a branch per row);
+      // windows of half a ring, to load one while the other is rounded, 171.
       uint32_t *row_max = reinterpret_cast<uint32_t *>(stat + p.G);  // [slots][chunk_rows]
       const bool one_row = (p.tpr & 31) == 0;  // a warp's threads share a row
+      const bool two_rows = p.tpr > 32 || p.tpr == 16;  // or lie in at most two
       const int first = __shfl_sync(0xFFFFFFFFu, row, 0);
       // One maximum per warp and row goes to shared memory (a warp holds one or
       // two rows, or several narrow ones; maxima do not depend on the order).
-      auto maxima = [&](const uint8_t *src, uint32_t *mx, int nb) {
+      auto maxima = [&](const uint8_t *src, uint32_t *mx, int nb, auto all) {
+        constexpr bool ALL = decltype(all)::value;
         uint32_t mb[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          float m = 0.0f;
-          if (k < nb) {
-            float2 z[H];
-            values(src, k, z);
+        for (int k = 0; k < K; ++k) mb[k] = 0u;
+        if (live) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) m = fmaxf(m, fmaxf(fabsf(z[h].x), fabsf(z[h].y)));
+          for (int k = 0; k < K; ++k) {
+            if (ALL || k < nb) {
+              float2 z[H];
+              values(src, k, z);
+              float m = 0.0f;
+#pragma unroll
+              for (int h = 0; h < H; ++h) m = fmaxf(m, fmaxf(fabsf(z[h].x), fabsf(z[h].y)));
+              mb[k] = __float_as_uint(m);
+            }
           }
-          mb[k] = __float_as_uint(m);
         }
         if (one_row) {
 #pragma unroll
@@ -739,7 +748,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
 #pragma unroll
             for (int k = 0; k < K; ++k) atomicMax(mx + row + k * p.rpi, mb[k]);
           }
-        } else if (p.tpr > 32) {
+        } else if (two_rows) {
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, row == first ? 0u : mb[k]);
@@ -754,40 +763,51 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
           for (int k = 0; k < K; ++k) atomicMax(mx + row + k * p.rpi, mb[k]);
         }
       };
-      auto codes = [&](const uint8_t *src, const uint32_t *mx, int nb, int64_t pix) {
+      auto codes = [&](const uint8_t *src, const uint32_t *mx, int nb, int64_t pix, auto all) {
+        constexpr bool ALL = decltype(all)::value;
+        static_assert(V == 8, "int8 rows are made of bf16 activations");
+        float r[K];
+        bool plain = true;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (k < nb) {
-            float2 z[H];
-            values(src, k, z);
-            // rint(y * (127 / amax)) in one fused step: y is a rounded fp32
-            // value already, so a quotient off by 2^-22 moves a code only
-            // where y is that close to a tie; the scale is the IEEE quotient.
-            // Next to the subnormals, where 127 / amax leaves fp32, and beyond
-            // 2^126, where the fast quotient is 0, divide.
-            const float amax = __uint_as_float(mx[row + k * p.rpi]);
-            uint32_t code[V];
-            if (amax >= 1e-30f && amax <= 1e37f) {
-              const float r = __fdividef(127.0f, amax);
+          r[k] = __uint_as_float(mx[row + k * p.rpi]);
+          if (ALL || k < nb) plain = plain && r[k] != 0.0f;
+        }
+        if (!ok) return;
+        uint2 *to = reinterpret_cast<uint2 *>(p.q + pix * p.C + vec * V);
+        const int64_t to_row = static_cast<int64_t>(p.rpi) * p.C / static_cast<int64_t>(sizeof(uint2));
+        if (plain) {
+          // rint(y * (127 / amax)) in one fused step: y is a rounded fp32
+          // value already, so a quotient off by 2^-22 moves a code only
+          // where y is that close to a tie; the scale is the IEEE quotient.
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            if (ALL || k < nb) {
+              float2 z[H];
+              values(src, k, z);
+              uint32_t code[V];
 #pragma unroll
               for (int h = 0; h < H; ++h) {
-                const float2 t = fma2_rn(z[h], make_float2(r, r), make_float2(kRintMagic, kRintMagic));
+                const float2 t = fma2_rn(z[h], make_float2(r[k], r[k]), make_float2(kRintMagic, kRintMagic));
                 code[2 * h] = __float_as_uint(t.x);
                 code[2 * h + 1] = __float_as_uint(t.y);
               }
-            } else {
-              const float sc = __fdiv_rn(amax, 127.0f);
+              to[k * to_row] = pack_codes(code);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < (ALL ? K : nb); ++k) {
+            const float sc = p.s_q[pix + k * p.rpi];  // this block's own, behind a barrier
+            float2 z[H];
+            values(src, k, z);
+            uint32_t code[V];
 #pragma unroll
-              for (int h = 0; h < H; ++h) {
-                code[2 * h] = sc == 0.0f ? 0u : quant_exact(z[h].x, sc);
-                code[2 * h + 1] = sc == 0.0f ? 0u : quant_exact(z[h].y, sc);
-              }
+            for (int h = 0; h < H; ++h) {
+              code[2 * h] = sc == 0.0f ? 0u : quant_exact(z[h].x, sc);
+              code[2 * h + 1] = sc == 0.0f ? 0u : quant_exact(z[h].y, sc);
             }
-            static_assert(V == 8, "int8 rows are made of bf16 activations");
-            if (ok) {
-              *reinterpret_cast<uint2 *>(p.q + (pix + k * p.rpi) * p.C + vec * V) = pack_codes(code);
-              if (vec == 0) p.s_q[pix + k * p.rpi] = __fdiv_rn(amax, 127.0f);
-            }
+            to[k * to_row] = pack_codes(code);
           }
         }
       };
@@ -799,16 +819,39 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
         int s = slot;
         for (int i = top; i >= low; --i) {
           if (i < chunks - NS) arrive_full(s);
-          maxima(norm_smem + s * slot_bytes + offset, row_max + s * chunk_rows,
-                 i == chunks - 1 ? last_nb : (live ? K : 0));
+          const uint8_t *src = norm_smem + s * slot_bytes + offset;
+          if (i < chunks - 1)
+            maxima(src, row_max + s * chunk_rows, K, std::true_type{});
+          else
+            maxima(src, row_max + s * chunk_rows, last_nb, std::false_type{});
+          s = s == 0 ? NS - 1 : s - 1;
+        }
+        __syncthreads();
+        // The rows' scales, and in place of a maximum the factor of its codes:
+        // 127 / amax, or 0 (divide) for a row of zeros, next to the subnormals,
+        // where the factor leaves fp32, and beyond 2^126, where the fast
+        // quotient is 0.
+        s = slot;
+        for (int i = top; i >= low; --i) {
+          const int r0 = i * chunk_rows;
+          for (int j = tid; j < chunk_rows && r0 + j < pixels; j += kNormThreads) {
+            const float amax = __uint_as_float(row_max[s * chunk_rows + j]);
+            if (ok) p.s_q[static_cast<int64_t>(b) * p.S + lo + r0 + j] = __fdiv_rn(amax, 127.0f);
+            row_max[s * chunk_rows + j] =
+                __float_as_uint(amax >= 1e-30f && amax <= 1e37f ? __fdividef(127.0f, amax) : 0.0f);
+          }
           s = s == 0 ? NS - 1 : s - 1;
         }
         __syncthreads();
         for (int i = top; i >= low; --i) {
           if (warp == 0 && i < top && i + 1 >= NS) fill(b, i + 1 - NS, slot + 1 == NS ? 0 : slot + 1);
-          codes(norm_smem + slot * slot_bytes + offset, row_max + slot * chunk_rows,
-                i == chunks - 1 ? last_nb : (live ? K : 0),
-                static_cast<int64_t>(b) * p.S + lo + static_cast<int64_t>(i) * chunk_rows + row);
+          const uint8_t *src = norm_smem + slot * slot_bytes + offset;
+          const int64_t pix = static_cast<int64_t>(b) * p.S + lo + static_cast<int64_t>(i) * chunk_rows + row;
+          if (i < chunks - 1) {
+            if (live) codes(src, row_max + slot * chunk_rows, K, pix, std::true_type{});
+          } else if (last_nb > 0) {
+            codes(src, row_max + slot * chunk_rows, last_nb, pix, std::false_type{});
+          }
           release(slot);
           slot = slot == 0 ? NS - 1 : slot - 1;
         }
