@@ -394,16 +394,14 @@ typedef enum { W8A8_ACT_NONE = 0, W8A8_ACT_SILU = 1 } w8a8_activation;
  * be dy or x itself with the same strides.  Sums run in a fixed order: equal
  * inputs give equal bits.
  * C % 8 == 0, C <= 4096 (2048 in fp32), strides of extents above 1 multiples
- * of 8 and at least C, B * S < 2^30, x, dy, y, q, weight, bias
- * 16-byte aligned.
+ * of 8 and at least C, B * S < 2^30, x, dy, y, q, weight, bias 16-byte aligned.
  * workspace: w8a8_group_norm_workspace_size bytes (0 for a forward form whose
- * samples take one block each), 16-byte aligned, no initialization needed; it must not be in
- * use by other work while the call runs.  One launch (the gradient of
- * parameters: two).  The blocks of a sample wait for one another, so they are
- * launched cooperatively and all run at once; every wait is bounded (see
- * w8a8_last_device_error), and after a launch that reported
- * W8A8_ERR_DEVICE_TIMEOUT, replaying a captured graph of it on the same
- * workspace is outside the contract.
+ * samples take one block each), 16-byte aligned, no initialization needed; it
+ * must not be in use by other work while the call runs.  One launch.  Its
+ * blocks wait for one another, so they are launched cooperatively and all run
+ * at once; every wait is bounded (see w8a8_last_device_error), and after a
+ * launch that reported W8A8_ERR_DEVICE_TIMEOUT, replaying a captured graph of
+ * it on the same workspace is outside the contract.
  */
 W8A8_API int w8a8_group_norm_workspace_size(int64_t B, int64_t S, int64_t C, int64_t G, int dtype,
                                             int backward, size_t *bytes);

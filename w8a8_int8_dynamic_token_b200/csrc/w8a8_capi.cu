@@ -1223,17 +1223,24 @@ int check_norm_strides(int64_t B, int64_t S, int64_t C, int64_t sb, int64_t ss) 
   return W8A8_OK;
 }
 
-// [entries | readers | channel sums]
+// [entries | readers | channel sums' entries | running channel sums]
 size_t norm_entry_bytes(const NormCut &c, int64_t B, int64_t G) {
   return c.slabs > 1 ? align256(static_cast<size_t>(B) * G * c.slabs * sizeof(uint4)) : 0;
 }
 size_t norm_reader_bytes(const NormCut &c, int64_t B) {
   return c.slabs > 1 ? align256(static_cast<size_t>(B) * c.slabs * sizeof(unsigned long long)) : 0;
 }
+size_t norm_channel_bytes(const NormCut &c, int64_t C) {
+  return align256(static_cast<size_t>(c.slabs) * c.teams * C * sizeof(uint4));
+}
+// The running sums count where samples outnumber the teams, of which a device
+// with fewer SMs has fewer.
 size_t norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, int dtype, bool backward) {
   const NormCut c = norm_cut(B, S, C, G, dtype, backward ? kNormBackward : kNormForward, kNormBlocks);
   return norm_entry_bytes(c, B, G) + norm_reader_bytes(c, B) +
-         (backward ? align256(static_cast<size_t>(B) * c.slabs * C * sizeof(float2)) : 0);
+         (backward ? norm_channel_bytes(c, C) +
+                         (B > 1 ? align256(static_cast<size_t>(c.slabs) * c.teams * C * sizeof(float2)) : 0)
+                   : 0);
 }
 
 void norm_params(NormParams *p, const NormCut &c, int64_t B, int64_t S, int64_t C, int64_t G,
@@ -1264,12 +1271,14 @@ void norm_params(NormParams *p, const NormCut &c, int64_t B, int64_t S, int64_t 
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   p->entries = reinterpret_cast<uint4 *>(ws);
   p->readers = reinterpret_cast<unsigned long long *>(ws + norm_entry_bytes(c, B, G));
-  p->chan = reinterpret_cast<float2 *>(ws + norm_entry_bytes(c, B, G) + norm_reader_bytes(c, B));
-  p->tag = c.slabs > 1 ? next_tag(48) : 0;
+  p->chan = reinterpret_cast<uint4 *>(ws + norm_entry_bytes(c, B, G) + norm_reader_bytes(c, B));
+  p->chan_run = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(p->chan) + norm_channel_bytes(c, C));
+  p->tag = next_tag(48);
 }
 
-// One launch.  Blocks that share a sample wait for one another, so the grid
-// (at most one block per SM) is launched cooperatively: all of it runs at once.
+// One launch.  Blocks that share a sample, or join dw and db, wait for one
+// another, so the grid (at most one block per SM) is launched cooperatively: all
+// of it runs at once.
 template <typename T, int MODE, bool SILU>
 int launch_norm_mode(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaStream_t stream) {
   const size_t region =
@@ -1296,7 +1305,7 @@ int launch_norm_mode(NormParams &p, const NormCut &c, const DeviceInfo &d, cudaS
   cfg.dynamicSmemBytes = static_cast<size_t>(slots * (slot + maxima)) + region;
   cfg.stream = stream;
   cfg.attrs = &attr;
-  cfg.numAttrs = c.slabs > 1 ? 1 : 0;
+  cfg.numAttrs = c.slabs > 1 || p.dweight != nullptr || p.dbias != nullptr ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
     cudaGetLastError();
     return W8A8_ERR_CUDA;
@@ -1312,11 +1321,8 @@ int launch_norm(NormParams &p, const NormCut &c, bool silu, const DeviceInfo &d,
 
 template <typename T>
 int launch_norm_grad(NormParams &p, const NormCut &c, bool silu, const DeviceInfo &d, cudaStream_t stream) {
-  int st = silu ? launch_norm_mode<T, kNormBackward, true>(p, c, d, stream)
-                : launch_norm_mode<T, kNormBackward, false>(p, c, d, stream);
-  if (st != W8A8_OK || (p.dweight == nullptr && p.dbias == nullptr)) return st;
-  return launch(norm_grad_params_kernel, dim3(static_cast<unsigned>(cdiv(p.C, 8))), dim3(256), 0,
-                stream, p);
+  return silu ? launch_norm_mode<T, kNormBackward, true>(p, c, d, stream)
+              : launch_norm_mode<T, kNormBackward, false>(p, c, d, stream);
 }
 
 template <bool FUSED, bool RAW>

@@ -34,6 +34,9 @@
 // Each block marks (tagged too) that it has read them; the sample's first block
 // waits for the marks beside its second pass and takes all tags back, so a
 // replayed graph, whose launches carry the same tag, finds none of its own.
+// The channels' sums of dw and db go the same way, one warp per channel reading
+// (and clearing) every block's entry after the second pass: a launch of their
+// own took 3 us more.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -81,7 +84,8 @@ struct NormParams {
   uint4 *entries;                    // [B][G][slabs] (slabs > 1)
   unsigned long long *readers;       // [B][slabs] (slabs > 1)
   unsigned long long tag;
-  float2 *chan;                      // [B][slabs][C]: channel sums (backward)
+  uint4 *chan;                       // [blocks][C]: entries of the channels' sums (backward)
+  float2 *chan_run;                  // [blocks][C]: the same over a block's samples so far (B > teams)
   float *mean_out, *rstd_out;        // [B, G] or nullptr
   const float *mean_in, *rstd_in;
   int8_t *q;
@@ -308,6 +312,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
   };
   const int row = tid / p.tpr, vec = tid - row * p.tpr;
   const bool live = row < p.rpi;
+  const bool parameters = BWD && (p.dweight != nullptr || p.dbias != nullptr);
   const int c = p.group_channels;
   const int group0 = vec * V / c, in0 = vec * V - group0 * c;  // the vector's first channel
   // Gradient: per channel rstd, -mean, weight and bias.  Loaded before the
@@ -518,7 +523,16 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
           t.x += region[r * p.C + ch].x;
           t.y += region[r * p.C + ch].y;
         }
-        if (ok) p.chan[(static_cast<int64_t>(b) * p.slabs + slab) * p.C + ch] = t;
+        if (ok && parameters) {
+          float2 all = t;  // over this block's samples
+          const int64_t at0 = static_cast<int64_t>(blockIdx.y * gridDim.x + slab) * p.C + ch;
+          if (b != static_cast<int>(blockIdx.y)) {
+            const float2 before = p.chan_run[at0];
+            all = make_float2(before.x + t.x, before.y + t.y);
+          }
+          if (b + p.teams < p.B) p.chan_run[at0] = all;
+          else entry_store(p.chan + at0, all, p.tag);
+        }
         float w = 1.0f;
         if (p.weight != nullptr)
           w = p.param_f32 ? __ldg(static_cast<const float *>(p.weight) + ch)
@@ -912,30 +926,48 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
       }
     }
   }
+  if constexpr (BWD) {
+    // dw and db: a warp per channel adds the blocks' sums in a fixed order.
+    // They were published after the blocks' first passes, so they are there;
+    // each is read once, and its tag goes with that.
+    const int blocks = gridDim.x * gridDim.y, block = blockIdx.y * gridDim.x + blockIdx.x;
+    for (int ch = block + warp * blocks; parameters && ch < p.C; ch += blocks * kNormWarps) {
+      constexpr int E = 5;  // entries a lane has under way at once
+      float a = 0.0f, d = 0.0f;
+#pragma unroll 1
+      for (int j0 = lane; j0 < blocks; j0 += 32 * E) {
+        float2 v[E];
+        unsigned long long tag[E];
+#pragma unroll
+        for (int u = 0; u < E; ++u) {
+          const int j = j0 + 32 * u;
+          tag[u] = p.tag;
+          v[u] = make_float2(0.0f, 0.0f);
+          if (j < blocks) tag[u] = entry_load(p.chan + static_cast<int64_t>(j) * p.C + ch, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < E; ++u) {
+          uint4 *const e = p.chan + static_cast<int64_t>(j0 + 32 * u) * p.C + ch;
+          if (tag[u] != p.tag && ok) ok = entry_wait(e, p.tag, v[u], &abort_flag);
+          if (ok && j0 + 32 * u < blocks) entry_store(e, make_float2(0.0f, 0.0f), 0ull);
+          a += v[u].x;
+          d += v[u].y;
+        }
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      a = warp_sum(a);
+      d = warp_sum(d);
+      if (lane == 0 && ok) {
+        if (p.dbias != nullptr) p.dbias[ch] = a;
+        if (p.dweight != nullptr) p.dweight[ch] = d;
+      }
+    }
+  }
   if (warp == 0 && !ok) {  // copies still in flight land before the block leaves
     for (int s = 0; s < NS; ++s) {
       volatile int never = 0;
       if (used & (1u << s)) mbar_wait(&full[s], (fill_par >> s) & 1u, &never);
     }
-  }
-}
-
-// dw and db: one warp per channel adds the slabs' sums in a fixed order.
-__global__ void __launch_bounds__(256) norm_grad_params_kernel(const __grid_constant__ NormParams p) {
-  const int ch = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (ch >= p.C) return;
-  float a = 0.0f, d = 0.0f;
-  const int64_t slots = static_cast<int64_t>(p.B) * p.slabs;
-  for (int64_t j = lane; j < slots; j += 32) {
-    const float2 t = p.chan[j * p.C + ch];
-    a += t.x;
-    d += t.y;
-  }
-  a = warp_sum(a);
-  d = warp_sum(d);
-  if (lane == 0) {
-    if (p.dbias != nullptr) p.dbias[ch] = a;
-    if (p.dweight != nullptr) p.dweight[ch] = d;
   }
 }
 
