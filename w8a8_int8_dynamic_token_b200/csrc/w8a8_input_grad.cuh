@@ -56,8 +56,9 @@ __device__ __forceinline__ uint2 grad_codes8(const float (&g)[8], float s, float
 
 constexpr int kGradThreads = 512;
 constexpr int kGradWarps = kGradThreads / 32;
-// A block per row (few rows, or very long ones); V > 0: the row's vectors stay
-// in registers (up to V per thread), V == 0: rows of any length in two passes.
+// A block per row (few rows, or very long ones); V > 0: the row's products stay
+// in registers (up to V vectors per thread), V == 0: rows of any length in two
+// passes.
 // The codes' rows are ldc bytes apart.
 template <int V>
 __global__ void __launch_bounds__(kGradThreads)
@@ -73,9 +74,10 @@ __global__ void __launch_bounds__(kGradThreads)
   grid_dependents_launch();
   grid_dependency_wait();
   clear_split_counters(counters, n_counters);
-  uint4 v[V > 0 ? V : 1];
+  float g[V > 0 ? V : 1][8];
   float m = 0.0f;
   if constexpr (V > 0) {
+    uint4 v[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int vi = tid + kGradThreads * j;
@@ -84,17 +86,13 @@ __global__ void __launch_bounds__(kGradThreads)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int vi = tid + kGradThreads * j;
-      if (vi < nvec) {
-        float g[8];
-        scale_vec8(v[j], s_w + 8 * vi, g);
-        m = absmax8(g, m);
-      }
+      scale_vec8(v[j], s_w + 8 * (vi < nvec ? vi : 0), g[j]);
+      m = absmax8(g[j], m);
     }
   } else {
     for (int vi = tid; vi < nvec; vi += kGradThreads) {
-      float g[8];
-      scale_vec8(__ldg(src + vi), s_w + 8 * vi, g);
-      m = absmax8(g, m);
+      scale_vec8(__ldg(src + vi), s_w + 8 * vi, g[0]);
+      m = absmax8(g[0], m);
     }
   }
   uint32_t mb = warp_max_u32(__float_as_uint(m), 32);
@@ -113,17 +111,12 @@ __global__ void __launch_bounds__(kGradThreads)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int vi = tid + kGradThreads * j;
-      if (vi < nvec) {
-        float g[8];
-        scale_vec8(v[j], s_w + 8 * vi, g);
-        dst[vi] = sc == 0.0f ? make_uint2(0u, 0u) : grad_codes8(g, sc, rc, fast);
-      }
+      if (vi < nvec) dst[vi] = sc == 0.0f ? make_uint2(0u, 0u) : grad_codes8(g[j], sc, rc, fast);
     }
   } else {
     for (int vi = tid; vi < nvec; vi += kGradThreads) {
-      float g[8];
-      scale_vec8(__ldcs(src + vi), s_w + 8 * vi, g);
-      dst[vi] = sc == 0.0f ? make_uint2(0u, 0u) : grad_codes8(g, sc, rc, fast);
+      scale_vec8(__ldcs(src + vi), s_w + 8 * vi, g[0]);
+      dst[vi] = sc == 0.0f ? make_uint2(0u, 0u) : grad_codes8(g[0], sc, rc, fast);
     }
   }
 }
