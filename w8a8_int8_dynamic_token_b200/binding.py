@@ -730,6 +730,15 @@ def _rotary_geometry(x_shape, x_strides, k_shape, k_strides, pos_shape, pos_stri
             _position_strides(pos_shape, pos_strides, batch, tokens, with_axes))
 
 
+def _rotary_out(x, heads, out):
+    """out, or a new tensor laid out as x, and its strides."""
+    if out is None:
+        out = torch.empty_like(x)
+        if x.is_contiguous():
+            return out, heads[1:]
+    return out, _head_strides(out.shape, out.stride(), "out")[1]
+
+
 def rotary(x, positions, inv_freq, k=None, layout="interleaved", axis=None, scale=1.0,
            backward=False, out=None, out_k=None, stream=None):
     """Rotary positions on heads x [tokens, heads, dim] or [batch, tokens, heads,
@@ -771,14 +780,12 @@ def rotary(x, positions, inv_freq, k=None, layout="interleaved", axis=None, scal
         with _switching(x.device, stream):
             return rotary(x, positions, inv_freq, k, layout, axis, scale, backward, out, out_k)
     x_heads, k_heads, sizes, pos = geometry
-    y = out if out is not None else torch.empty_like(x)
-    ys = _head_strides(y.shape, y.stride(), "out")[1]
+    y, ys = _rotary_out(x, x_heads, out)
     y_k = None
     if k is None:
         tensors = _ONE_HEADS(x.data_ptr(), y.data_ptr(), *x_heads, *ys)
     else:
-        y_k = out_k if out_k is not None else torch.empty_like(k)
-        ks = _head_strides(y_k.shape, y_k.stride(), "out_k")[1]
+        y_k, ks = _rotary_out(k, k_heads, out_k)
         tensors = _TWO_HEADS(x.data_ptr(), y.data_ptr(), *x_heads, *ys, k.data_ptr(),
                              y_k.data_ptr(), *k_heads, *ks)
     st = lib().w8a8_rotary(tensors, 1 if k is None else 2, _DTYPES[dtype], *sizes,
