@@ -20,6 +20,12 @@
 // the GPU) is read once; of longer ones the second pass, which runs backwards,
 // reads the rest again, the most recently read chunks first.
 //
+// Measured in a graph: 1048576 x 128 in bf16 with SiLU 149 us (537 MB once; 776
+// with what is read twice, 5.2 TB/s), twice as many pixels 282 (5.7 TB/s, the
+// same without SiLU: memory); 2 x 4096 x 1280 to int8 rows 23; gradient of 4 x
+// 4096 x 512 27.  Below the ring's size latency is what is left: 9 us for 2 x 64
+// x 1280 (launch, first loads, one exchange).
+//
 // Statistics: a thread keeps one 16-byte vector of channels; batches of rows
 // are reduced in two passes over registers (mean, then squared deviations)
 // and joined by the pairwise update of Chan, Golub and LeVeque (1979).  No
