@@ -528,6 +528,82 @@ def test_group_norm_on_two_streams_at_once():
         assert all(torch.equal(y, want) for y in ys)
 
 
+@pytest.mark.parametrize("shape,groups", [((2, 600, 64), 8), ((1, 9000, 48), 6), ((300, 5, 64), 8)])
+def test_group_norm_gradient_of_one_parameter_or_none(shape, groups):
+    x, w, b, (xd, wd, bd) = make_norm(shape, torch.bfloat16, "float", 0.0)
+    dy = torch.randn(shape, generator=gen(14)).bfloat16().cuda()
+    for wi, bi in ((wd, None), (None, bd), (None, None)):
+        _, mean, rstd = w8a8.group_norm(xd, groups, wi, bi, activation="silu", return_stats=True)
+        dx, dw, db = w8a8.group_norm_backward(dy, xd, mean, rstd, wi, bi, activation="silu")
+        x3, dy3 = x.view(shape), dy.cpu()
+        wx, ww, wb = grads64(dy3, x3, groups, None if wi is None else w, None if bi is None else b, mean.cpu(), rstd.cpu(), True)
+        close(dx, wx[0], wx[1], "dx")
+        assert (dw is None) == (wi is None) and (db is None) == (bi is None)
+        if dw is not None:
+            close(dw, *ww, "dweight")
+        if db is not None:
+            close(db, *wb, "dbias")
+
+
+def norm_calls(ws, x, dy, w, b):
+    y, mean, rstd = w8a8.group_norm(x, 8, w, b, activation="silu", return_stats=True, workspace=ws)
+    q, s = w8a8.group_norm_quant(x, 8, w, b, workspace=ws)
+    return (y, q, s, *w8a8.group_norm_backward(dy, x, mean, rstd, w, b, activation="silu", workspace=ws))
+
+
+def test_group_norm_graphs_that_share_a_workspace():
+    jobs, graphs = [], []
+    need = w8a8.group_norm_workspace_size(2, 3000, 64, 8, torch.bfloat16, True)
+    ws = torch.full((need,), 0x77, dtype=torch.uint8, device="cuda")
+    for i, shape in enumerate([(2, 3000, 64), (1, 2500, 64)]):
+        x, w, b, (xd, wd, bd) = make_norm(shape, torch.bfloat16, "same", 0.0, seed=50 + i)
+        dy = torch.randn(shape, generator=gen(52 + i)).bfloat16().cuda()
+        want = norm_calls(ws, xd, dy, wd, bd)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = norm_calls(ws, xd, dy, wd, bd)
+        jobs.append((want, got, (xd, wd, bd, dy)))  # the graph reads them: they have to live
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 0, 1):
+        want, got, _ = jobs[i]
+        for t in got:
+            t.zero_()
+        graphs[i].replay()
+        for a, c in zip(want, got):
+            assert torch.equal(a, c)
+
+
+def test_group_norm_on_branches_of_a_graph_and_streams_of_two_priorities():
+    # launches that may run at once, each with blocks that wait for one another
+    x, w, b, (xd, wd, bd) = make_norm((1, 30000, 64), torch.bfloat16, "same", 0.0)
+    dy = torch.randn((1, 30000, 64), generator=gen(54)).bfloat16().cuda()
+    want = norm_calls(None, xd, dy, wd, bd)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(priority=p) for p in (0, -1, 0)]
+    for _ in range(10):
+        got = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(norm_calls(None, xd, dy, wd, bd))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for one in got for a, c in zip(want, one))
+    main = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        got = []
+        for s in streams:
+            s.wait_stream(main)
+            with torch.cuda.stream(s):
+                got.append(norm_calls(None, xd, dy, wd, bd))
+        for s in streams:
+            main.wait_stream(s)
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert w8a8.last_device_error() == B.W8A8_OK
+    assert all(torch.equal(a, c) for one in got for a, c in zip(want, one))
+
+
 # ----------------------------------------------------------------- input gradient
 
 def input_grad_ref(dy, Wq, s_w):
