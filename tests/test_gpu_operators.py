@@ -631,7 +631,7 @@ GRAD_SHAPES = [
     (1, 8, 16), (1, 136, 128), (3, 4096, 4096), (16, 1000, 528), (17, 264, 144), (33, 520, 1040), (64, 256, 128),
     (129, 2056, 272), (300, 264, 256), (511, 1032, 2064), (700, 4096, 1024), (5, 13000, 256), (260, 24, 16),
     (1300, 520, 4112), (297, 8, 32), (600, 40, 64), (900, 5000, 128), (310, 12288, 32), (333, 9000, 16),
-    (2500, 2064, 256),
+    (2500, 2064, 256), (890, 12288, 32), (889, 8, 32), (1200, 40, 64), (1000, 9000, 16),
 ]
 
 
@@ -722,6 +722,8 @@ def test_linear_input_grad_extreme_scales():
     assert torch.equal(got.cpu(), input_grad_ref(dy, Wq, s_w)[0])
     few = w8a8.linear_input_grad(dy[:30].cuda(), Wq.cuda(), s_w.cuda())
     assert torch.equal(few.cpu(), got[:30].cpu())
+    many = w8a8.linear_input_grad(dy.repeat(4, 1).cuda(), Wq.cuda(), s_w.cuda())
+    assert torch.equal(many, got.repeat(4, 1))
 
 
 # ----------------------------------------------------------------- together

@@ -990,9 +990,11 @@ int launch_quant_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, const 
   const int64_t ldc = grad_code_stride(N);
   const dim3 grid(static_cast<unsigned>(M));
   const int n32 = static_cast<int>(N);
-  // The bulk kernel gives each SM whole rows; with fewer rows than two per SM a
-  // block per row spreads them wider.
-  if (N <= kQuantBulkMaxK && M >= 2 * d.sms) {
+  // A block per row, or, where that would take many waves, the bulk kernel.
+  // Whole calls in a graph, us, rows / bulk: 300 x 4096 x 12288 20.0 / 20.9, 512
+  // 28.0 / 29.2, 1024 42.1 / 42.1, 2048 80.5 / 79.0; 300 x 12288 x 4096 34.4 /
+  // 35.4, 768 46.4 / 46.4, 1024 47.8 / 46.7, 2048 97.4 / 93.8.
+  if (N <= kQuantBulkMaxK && M >= 6 * d.sms) {
     int gw = 1;
     while (gw < 4 && gw * kQuantBulkWarpElems < N) gw *= 2;
     const int64_t room = d.max_smem_optin - 2048;

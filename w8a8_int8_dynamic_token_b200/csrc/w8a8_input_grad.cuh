@@ -56,7 +56,7 @@ __device__ __forceinline__ uint2 grad_codes8(const float (&g)[8], float s, float
 
 constexpr int kGradThreads = 512;
 constexpr int kGradWarps = kGradThreads / 32;
-// A block per row (few rows, or very long ones); V > 0: the row's products stay
+// A block per row (up to several rows per SM, or very long ones); V > 0: the row's products stay
 // in registers (up to V vectors per thread), V == 0: rows of any length in two
 // passes.
 // The codes' rows are ldc bytes apart.
