@@ -178,6 +178,29 @@ def test_rotary_broadcast_input():
     assert torch.equal(y, w8a8.rotary(x.contiguous(), pos, freq))
 
 
+def test_rotary_calls_one_after_another_without_a_pause():
+    # each call starts while the one before it drains, and reads what that wrote
+    def chain(pause):
+        x, k = xs.clone(), ks.clone()
+        for i in range(12):
+            w8a8.rotary(x, pos, freq, k=k, layout="half", backward=i % 3 == 2, out=x, out_k=k)
+            pause()
+            h = w8a8.linear_input_grad(x.view(600, 512), Wq, s_w)
+            pause()
+            k = (k + h.view(600, 2, 128)) * 0.5
+            pause()
+        return x, k
+    g = gen(15)
+    xs, ks = (torch.randn((600, n, 128), generator=g).bfloat16().cuda() for n in (4, 2))
+    Wq = torch.randint(-9, 10, (512, 256), generator=g, dtype=torch.int8).cuda()
+    s_w = (torch.rand(512, generator=g) * 1e-2).cuda()
+    pos, freq = torch.arange(600, device="cuda"), w8a8.rotary_frequencies(128)[0]
+    want = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        got = chain(lambda: None)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_rotary_gradient_is_the_transpose():
     # <u, R x> = <R^T u, x> up to the roundings of both sides
     freq = w8a8.rotary_frequencies(64, scaling="ramp", factor=8.0, trained=512)

@@ -1165,8 +1165,8 @@ int launch_rotary_t(RotParams &p, bool copy_rest, cudaStream_t stream) {
   }
   p.block_tokens = static_cast<int32_t>(nt);
   const size_t smem = static_cast<size_t>(nt) * pairs * sizeof(float2);
-  return launch(rotary_kernel<T, VEC, HALF, WIDE>, dim3(static_cast<unsigned>(cdiv(total, nt))),
-                dim3(threads), smem, stream, p);
+  return launch_ex(true, rotary_kernel<T, VEC, HALF, WIDE>, dim3(static_cast<unsigned>(cdiv(total, nt))),
+                   dim3(threads), smem, stream, p);
 }
 
 template <typename T>
