@@ -749,6 +749,16 @@ def test_linear_input_grad_extreme_scales():
     assert torch.equal(many, got.repeat(4, 1))
 
 
+@pytest.mark.parametrize("M,N,K", [(3000, 12288, 32), (2400, 10240, 16), (2000, 9000, 64), (4000, 6144, 16), (5000, 2960, 16)])
+def test_linear_input_grad_rows_of_a_shared_ring(M, N, K):
+    # many rows per block in rings of 7, 9, 10 and 16 slots for 4, 8 and 16
+    # groups, against calls of few rows, which take a block per row
+    dy, Wq, s_w = (t.cuda() for t in make_grad(M, N, K, 28))
+    want = torch.cat([w8a8.linear_input_grad(dy[i:i + 500], Wq, s_w) for i in range(0, M, 500)])
+    for _ in range(10):
+        assert torch.equal(w8a8.linear_input_grad(dy, Wq, s_w), want)
+
+
 # ----------------------------------------------------------------- together
 
 def block(x, p, act_rows):

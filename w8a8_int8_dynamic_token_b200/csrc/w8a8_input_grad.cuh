@@ -128,12 +128,35 @@ __global__ void __launch_bounds__(kGradThreads)
 // 16-byte halves of a vector's eight (32-byte steps between lanes would
 // conflict in pairs); rows come through one ring of bulk copies that all
 // groups share.  A row is multiplied twice, for its maximum and for its codes.
+// A slot's rows belong to different groups where the slots are no multiple of
+// the groups (7 and 4 at 12288 values), and nothing else keeps the groups in
+// step, so a group can reach its row while the slot's copy two or more before
+// it is still under way; the barrier's parity alone would then let it through.
+// It therefore waits until the row's own copy has been asked for (`issued`),
+// which happens once the copy before it has landed, and only then for its phase.
 // 4352 x 12288 takes 37 us (160 MB of traffic: 28.7 as a bare stream of the same
 // reads and writes), bound by shared memory: 12 bytes an element, 18 us of it.
 // With the scales in registers instead (whole block on two rows at a time, one
 // barrier per two rows) it took 38, with two such teams 46.
 constexpr int kGradBulkWarps = 16;
 constexpr int kGradMaxSlots = 16;
+
+// Until `count` copies have been asked for in a slot (bounded as every wait).
+__device__ __forceinline__ bool issued_wait(volatile int *issued, int count, volatile int *abort_flag) {
+  if (*issued >= count) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (*issued >= count) return true;
+    if ((i & 31u) == 0u) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(&g_device_error, W8A8_DEVERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
 
 __global__ void __launch_bounds__(kGradBulkWarps * 32, 1)
     quant_grad_bulk_kernel(const uint16_t *__restrict__ dy, int M, int N, int64_t lddy,
@@ -144,6 +167,7 @@ __global__ void __launch_bounds__(kGradBulkWarps * 32, 1)
   __shared__ uint64_t bars[kGradMaxSlots];
   __shared__ uint32_t red[kGradBulkWarps];
   __shared__ int okf[kGradBulkWarps];
+  __shared__ volatile int issued[kGradMaxSlots];  // copies asked for so far
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = group_warps, groups = kGradBulkWarps / G;
@@ -156,7 +180,10 @@ __global__ void __launch_bounds__(kGradBulkWarps * 32, 1)
   const int stride = static_cast<int>(gridDim.x);
   const int mine = (M - static_cast<int>(blockIdx.x) + stride - 1) / stride;  // rows of this block
   if (threadIdx.x == 0) {
-    for (int s = 0; s < slots; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < slots; ++s) {
+      mbar_init(&bars[s], 1);
+      issued[s] = 0;
+    }
     abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -167,6 +194,7 @@ __global__ void __launch_bounds__(kGradBulkWarps * 32, 1)
     const int64_t row = static_cast<int64_t>(blockIdx.x) + static_cast<int64_t>(i) * stride;
     mbar_arrive_expect_tx(&bars[s], row_bytes);
     bulk_load_g2s(ring + s * row_bytes, dy + row * lddy, row_bytes, &bars[s]);
+    issued[s] = i / slots + 1;
   };
   if (threadIdx.x == 0)
     for (int i = 0; i < slots && i < mine; ++i) fill(i, i);
@@ -189,8 +217,9 @@ __global__ void __launch_bounds__(kGradBulkWarps * 32, 1)
   int i = group;
   bool ok = true;
   for (; i < mine; i += groups) {
-    const int slot = i % slots;
-    ok = mbar_wait(&bars[slot], static_cast<uint32_t>(i / slots) & 1u, &abort_flag);
+    const int slot = i % slots, phase = i / slots;
+    ok = issued_wait(&issued[slot], phase + 1, &abort_flag) &&
+         mbar_wait(&bars[slot], static_cast<uint32_t>(phase) & 1u, &abort_flag);
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (G > 1) {  // the group's warps leave together or not at all
       if (lane == 0) okf[warp] = ok ? 1 : 0;
@@ -259,12 +288,12 @@ __global__ void __launch_bounds__(kGradBulkWarps * 32, 1)
     if (G > 1) named_barrier_sync(1 + group, gthreads); else __syncwarp();
     if (t == 0 && i + slots < mine) fill(i + slots, slot);
   }
-  if (!ok && t == 0) {
-    // gave up: the copies that only this group could have waited for land
-    // before the block leaves
+  __syncthreads();  // nothing more is asked for
+  if (threadIdx.x == 0 && abort_flag != 0) {
+    // gave up: the copies in flight land before the block leaves
     volatile int never = 0;
-    for (int j = i; j < mine && j < i + slots; ++j)
-      if (j % groups == group) mbar_wait(&bars[j % slots], static_cast<uint32_t>(j / slots) & 1u, &never);
+    for (int s = 0; s < slots; ++s)
+      if (issued[s] > 0) mbar_wait(&bars[s], static_cast<uint32_t>(issued[s] - 1) & 1u, &never);
   }
 }
 
