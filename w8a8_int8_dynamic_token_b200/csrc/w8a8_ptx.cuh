@@ -117,6 +117,12 @@ __device__ __forceinline__ void grid_dependents_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Store with release semantics at GPU scope: what this thread did, and what a
+// block barrier put before it, comes before the store for whoever acquires it.
+__device__ __forceinline__ void st_release_gpu_u64(unsigned long long *p, unsigned long long v) {
+  asm volatile("st.release.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+
 // Load with acquire semantics at GPU scope (pairs with a fence + atomic
 // release by the writers of the data the value guards).
 __device__ __forceinline__ unsigned long long ld_acquire_gpu_u64(const unsigned long long *p) {
