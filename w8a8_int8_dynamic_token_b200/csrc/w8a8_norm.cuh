@@ -949,8 +949,10 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
         dst -= dst_chunk;
       }
     }
-    if (p.slabs > 1 && slab == 0 && ok) {
-      // once every block has read the sample's entries: their tags go
+    if (p.slabs > 1 && slab == 0) {
+      // Once every block has read the sample's entries, their tags go.  A wait
+      // may have given up in some threads only, so all of them come to the
+      // barrier.
       for (int j = tid; j < p.slabs && ok; j += kNormThreads) {
         unsigned long long *r = p.readers + static_cast<int64_t>(b) * p.slabs + j;
         const uint64_t t0 = global_timer_ns();
@@ -963,11 +965,10 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
         }
         if (ok) *reinterpret_cast<volatile unsigned long long *>(r) = 0ull;
       }
-      if (__syncthreads_and(ok)) {
+      ok = __syncthreads_and(ok);
+      if (ok) {
         uint4 *e = p.entries + static_cast<int64_t>(b) * p.G * p.slabs;
         for (int i = tid; i < p.G * p.slabs; i += kNormThreads) entry_store(e + i, make_float2(0.0f, 0.0f), 0ull);
-      } else {
-        ok = false;
       }
     }
   }
