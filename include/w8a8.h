@@ -380,7 +380,8 @@ typedef enum { W8A8_ACT_NONE = 0, W8A8_ACT_SILU = 1 } w8a8_activation;
  * of a sample and a pixel in elements), G groups of C / G adjacent channels:
  *   mean, var over a sample's S * C / G values of a group (fp32, var biased),
  *   z = (x - mean) / sqrt(var + eps) * weight[c] + bias[c],  y = z, or
- *   z * sigmoid(z) with W8A8_ACT_SILU; fp32 throughout, rounded once.
+ *   z * sigmoid(z) with W8A8_ACT_SILU (0 below z = -87.3, off by less than
+ *   2^-119); fp32 throughout, rounded once.
  * weight, bias: [C] in x's type or fp32 (param_dtype), or NULL (1 and 0).
  * mean_out, rstd_out: fp32 [B, G], or both NULL.
  * w8a8_group_norm: y in x's type; it may be x itself with the same strides.

@@ -382,6 +382,56 @@ def test_group_norm_quant_rows_at_the_ends_of_fp32(size):
     assert ((q.cpu().double() * s64 - y64).abs() <= s64 * (0.5 + 127 * 2 * U) + slack).all()
 
 
+# z of every size, as the bias under a weight of zero
+TAILS = [-0.5, -5.0, -20.0, -40.0, -43.5, -44.0, -50.0, -60.0, -75.0, -87.0, -88.0, -100.0, -1e3, -1e10, -1e20, -3e38,
+         0.0, 0.5, 5.0, 20.0, 44.0, 60.0, 90.0, 1e3, 1e20, 3e38, -30.0, -63.0, -64.0, -70.0, -80.0, -86.0]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_group_norm_silu_of_every_size(dtype):
+    z = torch.tensor(TAILS)
+    x = torch.randn((2, 3, 32), generator=gen(60)).to(dtype).cuda()
+    w = torch.zeros(32, device="cuda")
+    y = w8a8.group_norm(x, 4, w, z.cuda(), activation="silu")
+    z64 = z.double()
+    gate = torch.sigmoid(z64)
+    # the power's exponent is rounded (1.25 |z| U with its constant), the power
+    # itself is off by 4 U, 1 + e, its product, reciprocal (2) and three products
+    # by 8; below 2^-119 the gate is 0
+    slack = (z64 * gate).abs() * (1.25 * z64.abs() + 12) * U + 2.0 ** -119
+    close(y, (z64 * gate).expand_as(y), slack, "y")
+    # the gradient: of one pixel dbias is dz, s + z s (1 - s) times dy
+    one = x[:1, :1].contiguous()
+    _, mean, rstd = w8a8.group_norm(one, 4, w, z.cuda(), return_stats=True)
+    dy = torch.randn((1, 1, 32), generator=gen(61)).to(dtype)
+    _, _, db = w8a8.group_norm_backward(dy.cuda(), one, mean, rstd, w, z.cuda(), activation="silu")
+    d = gate * (1 + z64 * (1 - gate))
+    dslack = gate * (1 + z64.abs()) * (1.25 * z64.abs().clamp_max(1e3) + 16) * U
+    dslack[z64 > 100] = 16 * U  # 1 - s and with it z s (1 - s) is 0
+    close(db, dy[0, 0].double() * d, dy[0, 0].double().abs() * (dslack + U * d.abs() + 2.0 ** -118), "dbias")
+
+
+def test_group_norm_silu_of_large_negative_values_is_nothing():
+    x = torch.randn((1, 40, 32), generator=gen(62)).cuda()
+    w = torch.full((32,), 1e20, device="cuda")
+    z = w8a8.group_norm(x, 4, w)
+    y = w8a8.group_norm(x, 4, w, activation="silu")
+    assert (z < -1e10).any() and (y[z < -1e10] == 0).all() and torch.equal(y[z > 1e10], z[z > 1e10])
+
+
+def test_group_norm_quant_silu_of_negative_rows():
+    # every value of a row far below zero: the scale comes from gates near 2^-80
+    z = -50.0 - 0.5 * torch.arange(32.0)
+    x = torch.randn((1, 20, 32), generator=gen(63)).bfloat16().cuda()
+    q, s = w8a8.group_norm_quant(x, 4, torch.zeros(32, device="cuda"), z.cuda(), activation="silu")
+    y = z.double() * torch.sigmoid(z.double())
+    slack = y.abs() * (1.25 * z.double().abs() + 12) * U
+    amax = y.abs().max().expand(20)
+    close(s, amax / 127, slack.max() / 127 + 2 * U * amax / 127, "scales")
+    s64 = s.cpu().double()[:, None]
+    assert ((q.cpu().double() * s64 - y).abs() <= s64 * (0.5 + 127 * 2 * U) + slack).all()
+
+
 def test_group_norm_extents_of_one_have_no_stride():
     x = torch.randn((1, 9, 16), generator=gen(13)).bfloat16().cuda()
     want = w8a8.group_norm(x, 2)

@@ -20,10 +20,10 @@
 // the GPU) is read once; of longer ones the second pass, which runs backwards,
 // reads the rest again, the most recently read chunks first.
 //
-// Measured in a graph: 1048576 x 128 in bf16 with SiLU 149 us (537 MB once; 776
-// with what is read twice, 5.2 TB/s), twice as many pixels 282 (5.7 TB/s, the
+// Measured in a graph: 1048576 x 128 in bf16 with SiLU 150 us (537 MB once; 776
+// with what is read twice, 5.2 TB/s), twice as many pixels 285 (5.7 TB/s, the
 // same without SiLU: memory); 2 x 4096 x 1280 to int8 rows 23; gradient of 4 x
-// 4096 x 512 27.  Below the ring's size latency is what is left: 9 us for 2 x 64
+// 4096 x 512 26.5.  Below the ring's size latency is what is left: 9 us for 2 x 64
 // x 1280 (launch, first loads, one exchange).
 //
 // Statistics: a thread keeps one 16-byte vector of channels; batches of rows
@@ -194,19 +194,23 @@ __device__ __forceinline__ float &at(float2 (&v)[H], int i) {
   return (i & 1) ? v[i >> 1].y : v[i >> 1].x;
 }
 
-// sigmoid of two values: 1 / (1 + 2^(-z log2 e)) with one reciprocal for
-// both, 1 / a = b / (a b), since the special-function unit (16 a clock and SM)
-// is what a second pass of exp and reciprocal per value would wait for.  The
-// exponent stops at 63 so that the product stays finite: the gate of a value
-// below -43.6 is 2^-63 instead of something smaller.
+// sigmoid of two values: 1 / (1 + 2^(-z log2 e)).  The power may overflow: the
+// gate is then 0, as it is from z = -87.3 on, where it leaves fp32's normal
+// numbers (z * sigmoid(z) is off by less than 2^-119 there).  A reciprocal each:
+// one for both, 1 / a = b / (a b), takes a quarter less of the special-function unit
+// (16 a clock and SM), but needs its powers held below 2^63, which stops the gate
+// at 2^-63, or formed from |z|, whose selections cost more than they save
+// (1048576 x 128 forward: 150.2 us; 148.4 stopped, 155.6 from |z|; gradient of
+// 4 x 4096 x 512: 26.4, 26.6, 27.5).
 __device__ __forceinline__ float2 sigmoid2(float2 z) {
   const float2 t = mul2_rn(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-  float e0, e1, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fminf(t.x, 63.0f)));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fminf(t.y, 63.0f)));
-  const float2 d = add2_rn(make_float2(e0, e1), make_float2(1.0f, 1.0f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
-  return mul2_rn(make_float2(r, r), make_float2(d.y, d.x));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  const float2 d = add2_rn(e, make_float2(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  return r;
 }
 
 // Sum over the warp in a fixed order.
