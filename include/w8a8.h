@@ -386,8 +386,12 @@ typedef enum { W8A8_ACT_NONE = 0, W8A8_ACT_SILU = 1 } w8a8_activation;
  * mean_out, rstd_out: fp32 [B, G], or both NULL.
  * w8a8_group_norm: y in x's type; it may be x itself with the same strides.
  * w8a8_group_norm_quant: x bf16, C % 16 == 0; the rows of y (fp32, not
- * rounded to bf16 first) quantized as w8a8_quant_act does: q int8 [B * S, C]
- * dense and s_a fp32 [B * S], the operand of w8a8_linear.
+ * rounded to bf16 first) as int8: q [B * S, C] dense and s_a fp32 [B * S], the
+ * operand of w8a8_linear.  a = max|y| of the row, s_a = a / 127 (fp32, IEEE),
+ * q = rint(y * f) of the exact product with f = 127 / a (fp32, IEEE) for a in
+ * [1e-30, 1e37], else clamp(rint(y / s_a)), 0 in a row of zeros.  w8a8_quant_act
+ * divides everywhere: its codes of the same values can differ by one where
+ * y / s_a lies within 127 * 2^-23 of a tie.
  * w8a8_group_norm_backward: from dy, x and the forward's mean and rstd,
  *   dz = dy * y'(z),  dbias = sum dz,  dweight = sum dz * xh  (fp32 [C], or
  *   NULL),  dx = (weight dz - E(weight dz) - xh E(weight dz xh)) * rstd

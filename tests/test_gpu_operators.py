@@ -432,6 +432,34 @@ def test_group_norm_quant_silu_of_negative_rows():
     assert ((q.cpu().double() * s64 - y).abs() <= s64 * (0.5 + 127 * 2 * U) + slack).all()
 
 
+def test_group_norm_quant_scales_and_codes_bit_for_bit():
+    # values known exactly (the bias under a weight of zero), at ties of the
+    # quotient and up to two steps beside them
+    rng = np.random.default_rng(64)
+    x = torch.randn((1, 3, 4096), generator=gen(64)).bfloat16().cuda()
+    w = torch.zeros(4096, device="cuda")
+    for size in [*np.exp2(rng.uniform(-20, 20, 30)), 1e-37, 1e-33, 3e36, 2e38, 127.0, 63.5]:
+        amax = np.float32(size)
+        s = np.float32(amax / np.float32(127))
+        y = ((rng.integers(-127, 127, 4096) + 0.5) * np.float64(s)).astype(np.float32)
+        for _ in range(2):
+            y = np.where(rng.random(4096) < 0.4, np.nextafter(y, np.float32(rng.choice([-1, 1]) * np.inf)), y)
+        y = np.clip(y, -amax, amax)
+        y[rng.integers(4096)] = amax
+        if 1e-30 <= amax <= 1e37:  # the exact product of y with the rounded factor (48 bits: exact in 64)
+            want = np.rint(y.astype(np.float64) * np.float64(np.float32(127) / amax)).astype(np.int8)
+        else:
+            want = np.clip(np.rint(y / s), -127, 127).astype(np.int8)
+        q, s_a = w8a8.group_norm_quant(x, 32, w, torch.from_numpy(y).cuda())
+        assert (s_a.cpu().numpy() == s).all()
+        assert np.array_equal(q.cpu().numpy(), np.broadcast_to(want, (3, 4096))), size
+        # the quotient's codes are the same but next to ties: s is off by 2^-24
+        # of itself, f and the quotient as much
+        quotient = y.astype(np.float64) / np.float64(s)
+        far = np.abs(np.abs(quotient - np.trunc(quotient)) - 0.5) > 127 * 2.0 ** -23
+        assert (np.rint(quotient) == want)[far].all() and (np.abs(np.rint(quotient) - want) <= 1).all()
+
+
 def test_group_norm_extents_of_one_have_no_stride():
     x = torch.randn((1, 9, 16), generator=gen(13)).bfloat16().cuda()
     want = w8a8.group_norm(x, 2)
