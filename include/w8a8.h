@@ -307,7 +307,9 @@ W8A8_API int w8a16_linear(const void *x_bf16, int64_t M, int64_t K, int64_t ldx,
  *   c[m,n]  = clamp(rint(g[m,n] / s_g[m]), -127, 127)    (a row of zeros: 0)
  *   dx[m,k] = bf16_rne( (float)(sum_n c[m,n] * Wq[n,k]) * s_g[m] )
  *
- * the sum exact in int32.  The channel scales lie along the contraction, so
+ * the sum exact in int32.  A NaN in a row of g makes its row of dx NaN, an
+ * infinity makes it infinite or NaN; the other rows are not touched by it.
+ * The channel scales lie along the contraction, so
  * they enter the rows before these are quantized per token.  Wq is read as it
  * is stored (no transposed copy).  Preconditions as for w8a8_linear_fused,
  * with N <= 133144 (132104 with codes of -128) as the length of the sum and

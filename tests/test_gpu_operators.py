@@ -827,6 +827,25 @@ def test_linear_input_grad_extreme_scales():
     assert torch.equal(many, got.repeat(4, 1))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (20, 4096, 64), (20, 8192, 64), (300, 12288, 32), (20, 13000, 64),
+                                   (1000, 12288, 32), (900, 5000, 256), (900, 24, 16)])
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+def test_linear_input_grad_shows_what_is_not_finite(M, N, K, what):
+    # anywhere in a row, in any number of rows: all of that row, and no other
+    dy, Wq, s_w = make_grad(M, N, K, 29)
+    want = input_grad_ref(dy, Wq, s_w)[0]
+    rows = sorted({0, M // 3, M - 1})
+    for i, r in enumerate(rows):
+        dy[r, (i * N) // 3 + N // 4] = what
+    got = w8a8.linear_input_grad(dy.cuda(), Wq.cuda(), s_w.cuda()).cpu()
+    hit = torch.zeros(M, dtype=torch.bool)
+    hit[rows] = True
+    assert not torch.isfinite(got[hit].float()).any()
+    if math.isnan(what):
+        assert torch.isnan(got[hit].float()).all()
+    assert torch.equal(got[~hit], want[~hit])
+
+
 @pytest.mark.parametrize("M,N,K", [(3000, 12288, 32), (2400, 10240, 16), (2000, 9000, 64), (4000, 6144, 16), (5000, 2960, 16)])
 def test_linear_input_grad_rows_of_a_shared_ring(M, N, K):
     # many rows per block in rings of 7, 9, 10 and 16 slots for 4, 8 and 16

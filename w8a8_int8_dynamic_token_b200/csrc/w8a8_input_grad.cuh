@@ -13,6 +13,9 @@
 // kernels, which read Wq as it is stored (its columns contiguous: MN-major
 // operands, see B_MN / A_MN there), so no transposed copy is kept.
 //
+// A NaN in a row makes the row's scale and with it its whole dx NaN, an infinity
+// makes them infinite or NaN, so that a training loop sees both.
+//
 // The rows are bound by memory: 2 M N bytes of dy in, M N bytes of codes out.
 #pragma once
 
@@ -87,12 +90,14 @@ __global__ void __launch_bounds__(kGradThreads)
     for (int j = 0; j < V; ++j) {
       const int vi = tid + kGradThreads * j;
       scale_vec8(v[j], s_w + 8 * (vi < nvec ? vi : 0), g[j]);
-      m = absmax8(g[j], m);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = absmax_nan(m, g[j][i]);
     }
   } else {
     for (int vi = tid; vi < nvec; vi += kGradThreads) {
       scale_vec8(__ldg(src + vi), s_w + 8 * vi, g[0]);
-      m = absmax8(g[0], m);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = absmax_nan(m, g[0][i]);
     }
   }
   uint32_t mb = warp_max_u32(__float_as_uint(m), 32);
@@ -236,11 +241,11 @@ __global__ void __launch_bounds__(kGradBulkWarps * 32, 1)
       products(xs, v, g);
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        m0 = fmaxf(m0, fabsf(g[h].x));
-        m1 = fmaxf(m1, fabsf(g[h].y));
+        m0 = absmax_nan(m0, g[h].x);
+        m1 = absmax_nan(m1, g[h].y);
       }
     }
-    uint32_t mb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(m0, m1)));
+    uint32_t mb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(absmax_nan(m0, m1)));
     if (G > 1) {  // across the group's warps
       if (lane == 0) red[warp] = mb;
       named_barrier_sync(1 + group, gthreads);

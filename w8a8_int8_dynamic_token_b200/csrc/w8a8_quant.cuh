@@ -86,6 +86,14 @@ __device__ __forceinline__ float absmax8(const float (&x)[8], float m) {
   return m;
 }
 
+// max(m, |x|), a NaN where either is one (fmaxf drops it).  It comes out as a
+// positive one, above infinity's pattern: integer maxima keep it, too.
+__device__ __forceinline__ float absmax_nan(float m, float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
+  return r;
+}
+
 // 8 bf16 (one 16-byte vector) -> 8 int8 codes (8 bytes).  s > 0; y = RN(1/s);
 // fast = the row's scale is in the range where quant_fast is exact (a
 // row-uniform choice, so there is no divergence inside a row).
