@@ -393,7 +393,8 @@ typedef enum { W8A8_ACT_NONE = 0, W8A8_ACT_SILU = 1 } w8a8_activation;
  * q = rint(y * f) of the exact product with f = 127 / a (fp32, IEEE) for a in
  * [1e-30, 1e37], else clamp(rint(y / s_a)), 0 in a row of zeros.  w8a8_quant_act
  * divides everywhere: its codes of the same values can differ by one where
- * y / s_a lies within 127 * 2^-23 of a tie.
+ * y / s_a lies within 127 * 2^-23 of a tie.  A NaN in a row makes its s_a NaN,
+ * an infinity makes it infinite.
  * w8a8_group_norm_backward: from dy, x and the forward's mean and rstd,
  *   dz = dy * y'(z),  dbias = sum dz,  dweight = sum dz * xh  (fp32 [C], or
  *   NULL),  dx = (weight dz - E(weight dz) - xh E(weight dz xh)) * rstd

@@ -460,6 +460,21 @@ def test_group_norm_quant_scales_and_codes_bit_for_bit():
         assert (np.rint(quotient) == want)[far].all() and (np.abs(np.rint(quotient) - want) <= 1).all()
 
 
+@pytest.mark.parametrize("C", [16, 64, 320, 1280, 4096])  # one row, two and several a warp
+def test_group_norm_quant_shows_what_is_not_finite(C):
+    x, w, b, (xd, wd, bd) = make_norm((2, 37, C), torch.bfloat16, "float", 0.0)
+    q, s = w8a8.group_norm_quant(xd, 2, wd, bd, activation="silu")
+    bad = xd.clone()
+    bad[1, 5, C // 2 + 3] = math.nan  # one value spoils its sample's group, and so a part of every row
+    qb, sb = w8a8.group_norm_quant(bad, 2, wd, bd, activation="silu")
+    assert torch.isnan(sb[37:]).all() and torch.equal(sb[:37], s[:37]) and torch.equal(qb[:37], q[:37])
+    for value, silu in ((math.nan, None), (math.nan, "silu"), (math.inf, None), (-math.inf, None), (math.inf, "silu")):
+        odd = bd.clone()
+        odd[C - 1] = value
+        sb = w8a8.group_norm_quant(xd, 2, wd, odd, activation=silu)[1]
+        assert (torch.isnan(sb) if math.isnan(value) else torch.isinf(sb)).all()
+
+
 def test_group_norm_extents_of_one_have_no_stride():
     x = torch.randn((1, 9, 16), generator=gen(13)).bfloat16().cuda()
     want = w8a8.group_norm(x, 2)

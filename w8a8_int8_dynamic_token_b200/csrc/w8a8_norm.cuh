@@ -5,7 +5,8 @@
 //   mean = E x,  rstd = 1 / sqrt(E (x - mean)^2 + eps)
 //   z = (x - mean) * rstd * w + b,  y = z or z * sigmoid(z)
 // The int8 form quantizes each pixel's row of y (fp32, not rounded to bf16
-// first) for the W8A8 layer that follows: s = max|y| / 127, q = rint(y (127 / max|y|)).
+// first) for the W8A8 layer that follows: s = max|y| / 127, q = rint(y (127 / max|y|));
+// a NaN in a row makes its scale NaN.
 // Backward, with xh = (x - mean) * rstd, n = S * c and dz = dy * y'(z):
 //   dw = sum dz * xh,  db = sum dz   (over samples and pixels)
 //   dx = rstd * (w dz - (1/n) sum w dz - xh * (1/n) sum w dz xh)
@@ -799,7 +800,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
               values(src, k, z);
               float m = 0.0f;
 #pragma unroll
-              for (int h = 0; h < H; ++h) m = fmaxf(m, fmaxf(fabsf(z[h].x), fabsf(z[h].y)));
+              for (int h = 0; h < H; ++h) m = absmax_nan(absmax_nan(m, z[h].x), z[h].y);
               mb[k] = __float_as_uint(m);
             }
           }
