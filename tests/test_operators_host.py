@@ -168,6 +168,34 @@ def test_rotary_frequencies():
             w8a8.rotary_frequencies(*bad)
 
 
+@pytest.mark.parametrize("rot,base,factor,trained,fast,slow", [
+    (128, 10000.0, 4.0, 131072, 32.0, 1.0), (128, 100.0, 4.0, 4096, 32.0, 1.0), (64, 10000.0, 40.0, 4096, 32.0, 1.0),
+    (64, 1e6, 32.0, 32768, 32.0, 1.0), (2, 10.0, 2.0, 1000, 32.0, 1.0), (32, 2.0, 8.0, 10 ** 9, 32.0, 1.0),
+    (64, 10000.0, 4.0, 100, 32.0, 1.0), (64, 10000.0, 4.0, 5, 32.0, 1.0), (64, 10000.0, 4.0, 1, 32.0, 1.0),
+])
+def test_rotary_frequencies_ramp_whole_range(rot, base, factor, trained, fast, slow):
+    # pair j turns trained * base^(-2j / rot) / 2 pi times; solved for j, and
+    # the part divided grows linearly from there to there
+    f, _ = w8a8.rotary_frequencies(rot, base)
+    ramp, _ = w8a8.rotary_frequencies(rot, base, "ramp", factor, trained, fast, slow)
+    at = lambda turns: rot / 2 * math.log(trained / (2 * math.pi * turns)) / math.log(base)  # noqa: E731
+    low, high = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rot - 1)
+    for j in range(rot // 2):
+        turns = trained * f[j].item() / (2 * math.pi)
+        part = 1.0 - (ramp[j] / f[j]).item()
+        if turns <= slow and high <= j:
+            want = 1.0 - 1.0 / factor
+        elif j <= low:
+            want = 0.0
+        else:
+            want = (1.0 - 1.0 / factor) * min(1.0, (j - low) / (high - low))
+        assert math.isclose(part, want, abs_tol=1e-12), j
+        if turns > slow * base ** (2.0 / rot):   # by more than a pair: divided in part at most
+            assert part < 1.0 - 1.0 / factor or j >= rot - 1
+    if trained == 131072:  # the slowest pair turns 2.4 times
+        assert math.isclose((ramp[63] / f[63]).item(), 0.46, abs_tol=1e-12)
+
+
 # ----------------------------------------------------------------- group norm
 
 def norm(kind="norm", x=P, xb=64000, xs=64, dtype=0, Bn=2, S=1000, C=64, G=8, w=P, b=P, pdt=0, eps=1e-5, act=0, y=P, yb=64000,

@@ -650,8 +650,11 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = No
                  the slowest frequency by factor and keeps the fastest;
       "ramp"     pairs that turn more than `fast` times over the `trained`
                  positions are kept, those that turn less than `slow` times are
-                 divided by factor, a linear ramp over the pair index between;
-                 scale = 0.1 ln(factor) + 1.
+                 divided by factor, a linear ramp over the pair index between,
+                 from the whole index below the one to the whole index above
+                 the other.  These ends lie within [0, rot - 1], so the upper
+                 one may be past the last pair, which then is only partly
+                 divided.  scale = 0.1 ln(factor) + 1.
     """
     if rot < 2 or rot % 2:
         raise ValueError("rot must be even and at least 2")
@@ -674,8 +677,11 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = No
     # the pair that turns t times over the trained positions
     low, high = (rot * math.log(trained / (t * 2.0 * math.pi)) / (2.0 * math.log(base))
                  for t in (fast, slow))
-    low, high = max(math.floor(low), 0), min(math.ceil(high), rot // 2 - 1)
-    ramp = ((i - low) / max(high - low, 0.001)).clamp(0.0, 1.0)
+    low, high = max(math.floor(low), 0), min(math.ceil(high), rot - 1)
+    if high <= 0:  # no pair turns `slow` times
+        ramp = torch.ones_like(i)
+    else:
+        ramp = ((i - low) / max(high - low, 0.001)).clamp(0.0, 1.0)
     return freq * (1.0 - ramp) + freq / factor * ramp, 0.1 * math.log(factor) + 1.0
 
 
