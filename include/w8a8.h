@@ -354,11 +354,12 @@ typedef struct {
  *   t = p[axis[i]] * inv_freq[i];
  * the other dim - rot values are copied.  backward != 0: the gradient of that
  * map, its transpose (t -> -t).  Rotations are fp32, rounded once; angles are
- * reduced exactly as 64-bit fixed-point turns, so far positions lose nothing.
+ * 64-bit fixed-point turns, off by at most |p| * 2^-65 turns (1.2e-8 radians at
+ * 2^36) before sine and cosine are taken in fp32.
  * positions: device integers of position_bits (32 or 64) bits, signed,
  * [batch, tokens, axes] with strides pos_batch and pos_token (in elements, 0
  * to share) and adjacent axes; axes 1..8.  inv_freq: HOST array of rot / 2
- * radians per position (finite, >= 0), any scaling for long contexts applied;
+ * radians per position (0 <= f < 2^64), any scaling for long contexts applied;
  * axis: HOST array of rot / 2 axis indices, or NULL (all 0).  Both are read
  * before the call returns.
  * y is x itself with the same strides, or does not overlap it (nor another

@@ -8,6 +8,7 @@ type), and the fp32 work ahead of it is off by a stated number of units of
 from __future__ import annotations
 
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -153,6 +154,39 @@ def test_rotary_far_positions_and_a_shared_row_of_them():
     slack = ROT_SLACK * (a.abs() + b.abs())
     close(y[..., :32], a * c - b * s, slack, "a")
     close(y[..., 32:], a * s + b * c, slack, "b")
+
+
+def two_pi():
+    """2 pi to 200 bits: Machin's 16 atan(1/5) - 4 atan(1/239), in whole numbers."""
+    one = 1 << 230
+
+    def atan(n):
+        total, power, k = 0, one // n, 1
+        while power:
+            total += power // k if k % 4 == 1 else -(power // k)
+            power //= n * n
+            k += 2
+        return total
+    return Fraction(2 * (16 * atan(5) - 4 * atan(239)), one)
+
+
+@pytest.mark.parametrize("far", [2 ** 20, 2 ** 33, 2 ** 36, 2 ** 38])
+def test_rotary_far_positions_against_whole_numbers(far):
+    # turns of pos * f from the exact product and a long 2 pi: the kernel's are
+    # off by |pos| 2^-65 at most
+    rng = np.random.default_rng(far)
+    freq = torch.from_numpy(np.concatenate([w8a8.rotary_frequencies(64, 1000000.0)[0].numpy(), rng.random(30), [6.5, 1e5]]))
+    pos = [far, -far, far - 1, far // 3, -far + 12345]
+    turn = two_pi()
+    ang = torch.tensor([[float(Fraction(f) * p / turn % 1) * (2 * math.pi) for f in freq.tolist()] for p in pos],
+                       dtype=torch.float64)
+    x = torch.randn((1, len(pos), 3, 128), generator=gen(65))
+    y = w8a8.rotary(x.cuda(), torch.tensor(pos).cuda(), freq, layout="half")
+    c, s = ang.cos()[None, :, None], ang.sin()[None, :, None]
+    a, b = x[..., :64].double(), x[..., 64:].double()
+    slack = (ROT_SLACK + far * 2.0 ** -65 * 2 * math.pi) * (a.abs() + b.abs())
+    close(y[..., :64], a * c - b * s, slack, "a")
+    close(y[..., 64:], a * s + b * c, slack, "b")
 
 
 def test_rotary_in_place_partial_and_out():

@@ -112,6 +112,11 @@ def test_rotary_refusals(change, expect):
     assert rotary(**change) == expect
 
 
+@pytest.mark.parametrize("f", [2.0 ** 64, 1e290, 1.7e308, -5e-324])
+def test_rotary_refuses_frequencies_that_have_no_turns(f):
+    assert rotary(freq=doubles(f)) == INV
+
+
 def test_rotary_python_checks():
     x, pos, freq = torch.zeros((4, 2, 16)), torch.arange(4), torch.ones(8, dtype=torch.float64)
     with pytest.raises(ValueError, match="CUDA"):

@@ -1125,13 +1125,28 @@ int launch_input_grad_swap(const w8a8_plan &plan, const int8_t *codes, const flo
 
 inline int dtype_size(int dtype) { return dtype == W8A8_DTYPE_FP32 ? 4 : 2; }
 
-// Turns per position * 2^64 (modulo whole turns) of a frequency in radians per
-// position, finite and >= 0.
+// Turns per position * 2^64 (modulo whole turns), to the nearest whole number, of
+// a frequency in radians per position: 0 <= radians < 2^64.  A product of 64-bit
+// floats would carry 53 bits, 2^-56 turns a position; here the 53 bits of the
+// frequency meet the first 192 fractional bits of 1 / (2 pi) in whole numbers.
 unsigned long long turns_q64(double radians) {
-  constexpr double kWhole = 18446744073709551616.0;  // 2^64
-  double v = radians * (kWhole / 6.283185307179586476925286766559);
-  if (v >= kWhole) v = std::fmod(v, kWhole);
-  return static_cast<unsigned long long>(v);
+  constexpr unsigned long long kInv2Pi[3] = {0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull,
+                                             0x28be60db9391054aull};  // least significant first
+  unsigned long long word;
+  std::memcpy(&word, &radians, sizeof(word));
+  const int exponent = static_cast<int>(word >> 52) & 0x7FF;
+  // radians = m * 2^(exponent - 1075); times 2^64 / (2 pi) = m * I * 2^-shift
+  // with I = floor(2^192 / (2 pi))
+  const int shift = 1075 + 128 - exponent;  // 117 or more
+  if (shift > 256) return 0ull;             // below 2^-75 (zero and subnormals too)
+  const unsigned long long m = (word & ((1ull << 52) - 1)) | (1ull << 52);
+  using Wide = unsigned __int128;
+  const Wide low = ((static_cast<Wide>(m) * kInv2Pi[0]) >> 64) + static_cast<Wide>(m) * kInv2Pi[1];
+  const Wide high = static_cast<Wide>(m) * kInv2Pi[2] + (low >> 64);  // m * I >> 128
+  // bits [shift, shift + 64) of m * I, rounded by the bit below them
+  const Wide cut = shift > 128 ? high >> (shift - 129)
+                               : ((high << 64) | static_cast<unsigned long long>(low)) >> (shift - 65);
+  return static_cast<unsigned long long>((cut + 1) >> 1);
 }
 
 // Whether rows that start at p and lie `strides` apart allow 16-byte accesses.
@@ -2017,7 +2032,7 @@ int w8a8_rotary(const w8a8_rotary_heads *tensors, int num_tensors, int dtype, in
   p.scale = scale;
   p.backward = backward ? 1 : 0;
   for (int64_t i = 0; i < rot / 2; ++i) {
-    if (!std::isfinite(inv_freq[i]) || inv_freq[i] < 0.0) return W8A8_ERR_INVALID_ARG;
+    if (!(inv_freq[i] >= 0.0 && inv_freq[i] < 18446744073709551616.0)) return W8A8_ERR_INVALID_ARG;  // 2^64
     const int32_t a = axis ? axis[i] : 0;
     if (a < 0 || a >= axes) return W8A8_ERR_INVALID_ARG;
     p.freq[i] = turns_q64(inv_freq[i]);

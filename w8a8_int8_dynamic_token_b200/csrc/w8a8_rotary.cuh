@@ -8,9 +8,10 @@
 // (t -> -t, the same scale).
 //
 // Angles.  A 32-bit product pos * f loses the angle of far positions, so the
-// frequencies are held as turns per position in 64-bit fixed point: pos * f
-// modulo one turn is then one wrapping 64-bit integer product, off by at most
-// |pos| * 2^-65 turns (1.5e-9 at 2^36), and its top 32 bits go to sincospif.
+// frequencies are held as turns per position in 64-bit fixed point, rounded to the
+// nearest (with 1 / (2 pi) in 192 bits, see turns_q64): pos * f modulo one turn is
+// then one wrapping 64-bit integer product, off by at most |pos| * 2^-65 turns
+// (1.2e-8 radians at 2^36), and its top 32 bits go to sincospif.
 //
 // Bound by memory: every value is read once and written once.  A block takes
 // one or a few tokens.  Each thread keeps one place within the head and one
