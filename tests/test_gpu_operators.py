@@ -189,6 +189,24 @@ def test_rotary_far_positions_against_whole_numbers(far):
     close(y[..., 64:], a * s + b * c, slack, "b")
 
 
+def test_rotary_cosines_and_sines():
+    # of pairs (1, 0) and (0, 1).  The angle is off by half a step of fp32 below a
+    # quarter of a half turn (pi 2^-27) and its cut at 2^-32 turns, cosine and sine
+    # by a step of their own
+    freq = torch.rand(64, generator=gen(66), dtype=torch.float64) * 4
+    pos = torch.arange(-3000, 3000)
+    x = torch.zeros((6000, 2, 128))
+    x[:, 0, :64] = 1.0
+    x[:, 1, 64:] = 1.0
+    ang = pos.double()[:, None] * freq
+    c, s = ang.cos(), ang.sin()
+    slack = lambda v: math.pi * (2.0 ** -27 + 2.0 ** -31) + 2.0 ** -23 * v.abs()  # noqa: E731
+    for sign, back in ((1.0, False), (-1.0, True)):
+        y = w8a8.rotary(x.cuda(), pos.cuda(), freq, layout="half", backward=back).cpu().double()
+        for got, want in ((y[:, 0, :64], c), (y[:, 0, 64:], sign * s), (y[:, 1, :64], -sign * s), (y[:, 1, 64:], c)):
+            assert ((got - want).abs() <= slack(want)).all()
+
+
 def test_rotary_in_place_partial_and_out():
     freq = w8a8.rotary_frequencies(32)[0]
     x = torch.randn((9, 4, 64), generator=gen(6)).bfloat16().cuda()

@@ -11,7 +11,8 @@
 // frequencies are held as turns per position in 64-bit fixed point, rounded to the
 // nearest (with 1 / (2 pi) in 192 bits, see turns_q64): pos * f modulo one turn is
 // then one wrapping 64-bit integer product, off by at most |pos| * 2^-65 turns
-// (1.2e-8 radians at 2^36), and its top 32 bits go to sincospif.
+// (1.2e-8 radians at 2^36).  Its top 32 bits are taken relative to the nearest
+// quarter turn, which leaves sincospif an angle off by 2.4e-8 radians at most.
 //
 // Bound by memory: every value is read once and written once.  A block takes
 // one or a few tokens.  Each thread keeps one place within the head and one
@@ -165,11 +166,20 @@ __global__ void __launch_bounds__(kRotThreads, 2)
     const long long pos = p.pos_is_64 ? static_cast<const long long *>(p.pos)[off]
                                       : static_cast<const int *>(p.pos)[off];
     const unsigned long long turns = static_cast<unsigned long long>(pos) * p.freq[pair];
-    // signed fraction of a turn in [-1/2, 1/2), twice it in half turns
-    const float half_turns = static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f;
+    // the nearest quarter turn, and the rest in half turns (within a quarter of
+    // one: four times as fine in fp32 as the whole angle)
+    const uint32_t hi = static_cast<uint32_t>(turns >> 32);
+    const uint32_t quarter = (hi + (1u << 29)) >> 30;
+    const int rest = static_cast<int>(hi - (quarter << 30));
     float s, c;
-    sincospif(half_turns, &s, &c);
-    turn[i] = make_float2(c * p.scale, (p.backward ? -s : s) * p.scale);
+    sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &s, &c);
+    if (quarter & 1u) {
+      const float t = c;
+      c = -s;
+      s = t;
+    }
+    const float turned = quarter & 2u ? -p.scale : p.scale;
+    turn[i] = make_float2(c * turned, (p.backward ? -s : s) * turned);
   }
   __syncthreads();
   if (!active) return;
