@@ -313,11 +313,12 @@ W8A8_API int w8a16_linear(const void *x_bf16, int64_t M, int64_t K, int64_t ldx,
  * they enter the rows before these are quantized per token.  Wq is read as it
  * is stored (no transposed copy).  Preconditions as for w8a8_linear_fused,
  * with N <= 133144 (132104 with codes of -128) as the length of the sum and
- * lddy, lddx multiples of 8.  variant: a w8a8_variant; AUTO chooses.  GEMV
- * and GEMM_BN64 have no such form (W8A8_ERR_UNSUPPORTED_SHAPE), GEMV_TC serves
- * M <= 128.  workspace: w8a8_input_grad_workspace_size bytes, 16-byte aligned
- * (codes and row scales, required, and the K-split region of w8a8_linear,
- * optional); no initialization is needed.
+ * lddy, lddx multiples of 8 (not looked at for one row).  variant: a
+ * w8a8_variant; AUTO chooses.  GEMV and GEMM_BN64 have no such form
+ * (W8A8_ERR_UNSUPPORTED_SHAPE), GEMV_TC serves M <= 128.  workspace:
+ * w8a8_input_grad_workspace_size bytes, 16-byte aligned (codes and row scales,
+ * required, and the K-split region of w8a8_linear, optional); no
+ * initialization is needed.
  */
 W8A8_API int w8a8_input_grad_workspace_size(int64_t M, int64_t N, int64_t K, int variant,
                                             size_t *bytes);

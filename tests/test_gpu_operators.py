@@ -836,6 +836,18 @@ def test_linear_input_grad_strides_and_out():
     assert (big == 9).all()
 
 
+def test_linear_input_grad_one_row_has_no_stride():
+    dy, Wq, s_w = make_grad(1, 64, 48, 30)
+    want = input_grad_ref(dy, Wq, s_w)[0]
+    column = dy.cuda().view(64, 1).t()  # [1, 64] with strides (1, 1)
+    assert column.stride(0) == 1
+    assert torch.equal(w8a8.linear_input_grad(column, Wq.cuda(), s_w.cuda()).cpu(), want)
+    out = torch.as_strided(torch.empty(64, dtype=torch.bfloat16, device="cuda"), (1, 48), (3, 1))
+    for odd in (0, 7, 64):
+        row = torch.as_strided(dy.cuda(), (1, 64), (odd, 1))
+        assert torch.equal(w8a8.linear_input_grad(row, Wq.cuda(), s_w.cuda(), out=out).cpu(), want)
+
+
 def test_linear_input_grad_against_the_unrounded_product():
     # every code stands within half a step of its value: the product is off by
     # at most s_g / 2 * sum |Wq| and its own rounding

@@ -45,6 +45,13 @@ def test_input_grad_refusals(change, expect):
     assert grad(**change) == expect
 
 
+def test_input_grad_one_row_has_no_stride():
+    # the strides are let through: the next refusal is the workspace's
+    for change in ({"lddy": 1}, {"lddx": 0}, {"lddy": 36, "lddx": 20}):
+        assert grad(M=1, ws=None, **change) == WS
+        assert grad(M=2, ws=None, **change) in (INV, SHAPE)
+
+
 def test_input_grad_workspace():
     # codes in rows of a multiple of 16 and the scales
     assert w8a8.input_grad_workspace_size(5, 24, 16) >= 5 * 32 + 5 * 4

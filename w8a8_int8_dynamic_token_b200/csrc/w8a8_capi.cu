@@ -1938,6 +1938,10 @@ int w8a8_linear_input_grad(const void *dy, int64_t M, int64_t N, int64_t lddy, c
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (!dy || !Wq || !s_w || !dx) return W8A8_ERR_INVALID_ARG;
   if (variant < W8A8_VARIANT_AUTO || variant > W8A8_VARIANT_GEMV_TC) return W8A8_ERR_INVALID_ARG;
+  if (M == 1) {  // one row has no stride
+    lddy = N;
+    lddx = K;
+  }
   int st = check_input_grad(M, N, K, lddy, lddx);
   if (st != W8A8_OK) return st;
   if (!aligned16(dy) || !aligned16(Wq) || !aligned16(s_w) || !aligned16(dx))
