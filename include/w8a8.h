@@ -338,7 +338,7 @@ typedef enum {
 
 /* The heads of one tensor, [batch, tokens, heads, dim] with adjacent values
  * in a head and any strides (in elements) otherwise; x strides may be 0 (a
- * broadcast input), y strides of extents above 1 may not. */
+ * broadcast input), y strides of extents above 1 are at least dim in size. */
 typedef struct {
     const void *x;
     void *y;

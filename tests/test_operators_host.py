@@ -119,6 +119,15 @@ def test_rotary_refusals(change, expect):
     assert rotary(**change) == expect
 
 
+@pytest.mark.parametrize("change", [{"y_head": 15}, {"y_head": 1}, {"y_head": -8}, {"y_token": 8}, {"y_token": -15}, {"y_batch": 12}])
+def test_rotary_refuses_outputs_that_share_values(change):
+    batch = 2 if "y_batch" in change else 1
+    assert rotary(batch=batch, heads=({"y_batch": 128, **change},)) == INV
+    assert rotary(batch=batch, heads=({"y_batch": 128}, {"y_batch": 128, **change})) == INV
+    # an extent of one has no stride: the next refusal is the alignment's
+    assert rotary(batch=1, tokens=1, heads=({"heads": 1, "y": 257, **change},)) == ALIGN
+
+
 @pytest.mark.parametrize("f", [2.0 ** 64, 1e290, 1.7e308, -5e-324])
 def test_rotary_refuses_frequencies_that_have_no_turns(f):
     assert rotary(freq=doubles(f)) == INV

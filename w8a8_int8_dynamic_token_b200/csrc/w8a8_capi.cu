@@ -2006,8 +2006,9 @@ int w8a8_rotary(const w8a8_rotary_heads *tensors, int num_tensors, int dtype, in
     const w8a8_rotary_heads &t = tensors[i];
     if (!t.x || !t.y || t.heads < 1) return W8A8_ERR_INVALID_ARG;
     if (t.heads > INT32_MAX / 4) return W8A8_ERR_UNSUPPORTED_SHAPE;
-    // every head of y is a place of its own
-    if ((batch > 1 && t.y_batch == 0) || (tokens > 1 && t.y_token == 0) || (t.heads > 1 && t.y_head == 0))
+    // every head of y is a place of its own: less than a head apart, two share values
+    auto close = [dim](int64_t extent, int64_t stride) { return extent > 1 && stride < dim && stride > -dim; };
+    if (close(batch, t.y_batch) || close(tokens, t.y_token) || close(t.heads, t.y_head))
       return W8A8_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(t.x) % size != 0 || reinterpret_cast<uintptr_t>(t.y) % size != 0)
       return W8A8_ERR_MISALIGNED;
