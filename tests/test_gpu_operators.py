@@ -253,6 +253,22 @@ def test_rotary_calls_one_after_another_without_a_pause():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_rotary_extents_of_one_have_no_stride():
+    freq = w8a8.rotary_frequencies(64)[0]
+    x = torch.randn((1, 9, 4, 64), generator=gen(67)).bfloat16().cuda()
+    pos = torch.arange(9, device="cuda")
+    want = w8a8.rotary(x, pos, freq, layout="half")
+    for shape, strides, at in (((1, 9, 4, 64), (3, 256, 64, 1), pos), ((9, 1, 4, 64), (256, 5, 64, 1), pos[:, None]),
+                               ((1, 36, 1, 64), (1, 64, 7, 1), pos.repeat_interleave(4))):
+        out = torch.zeros_like(x)
+        w8a8.rotary(torch.as_strided(x, shape, strides), at, freq, layout="half", out=torch.as_strided(out, shape, strides))
+        assert torch.equal(out, want)
+        same = x.clone()
+        view = torch.as_strided(same, shape, strides)
+        w8a8.rotary(view, at, freq, layout="half", out=view)
+        assert torch.equal(same, want)
+
+
 def test_rotary_gradient_is_the_transpose():
     # <u, R x> = <R^T u, x> up to the roundings of both sides
     freq = w8a8.rotary_frequencies(64, scaling="ramp", factor=8.0, trained=512)

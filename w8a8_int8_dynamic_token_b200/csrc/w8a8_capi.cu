@@ -2016,13 +2016,13 @@ int w8a8_rotary(const w8a8_rotary_heads *tensors, int num_tensors, int dtype, in
     r.x = t.x;
     r.y = t.y;
     r.heads = static_cast<int32_t>(t.heads);
-    r.xb = t.x_batch; r.xt = t.x_token; r.xh = t.x_head;
-    r.yb = t.y_batch; r.yt = t.y_token; r.yh = t.y_head;
+    // an extent of one has no stride
+    auto stride = [](int64_t extent, int64_t v) { return extent > 1 ? v : 0; };
+    r.xb = stride(batch, t.x_batch); r.xt = stride(tokens, t.x_token); r.xh = stride(t.heads, t.x_head);
+    r.yb = stride(batch, t.y_batch); r.yt = stride(tokens, t.y_token); r.yh = stride(t.heads, t.y_head);
     heads += t.heads;
-    wide = wide && wide_rows(t.x, t.x_batch, t.x_token, t.x_head, vec) &&
-           wide_rows(t.y, t.y_batch, t.y_token, t.y_head, vec);
-    in_place = in_place && t.x == t.y && t.x_batch == t.y_batch && t.x_token == t.y_token &&
-               t.x_head == t.y_head;
+    wide = wide && wide_rows(t.x, r.xb, r.xt, r.xh, vec) && wide_rows(t.y, r.yb, r.yt, r.yh, vec);
+    in_place = in_place && t.x == t.y && r.xb == r.yb && r.xt == r.yt && r.xh == r.yh;
   }
   p.total_heads = static_cast<int32_t>(heads);
   p.batch = static_cast<int32_t>(batch);
