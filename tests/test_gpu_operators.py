@@ -683,6 +683,41 @@ def test_group_norm_longer_than_the_ring(shape, groups, dtype, pad):
         assert (wide[..., C:] == 0).all()
 
 
+def joins(B, S, C, G, dtype):
+    """Roundings one after another in a statistic, from the kernel's own cut: a
+    sample has 148 / B blocks (one at least), a block 512 threads on vectors of 16
+    bytes, a thread batches of 4 rows that join one by one; then the threads' and
+    the blocks' values join over 32 lanes."""
+    row_threads = C * dtype.itemsize // 16
+    rows = min(512 // row_threads, S)
+    blocks = min(max(148 // B, 1), math.ceil(S / (4 * rows)))
+    return math.ceil(math.ceil(S / blocks) / (4 * rows)) + 4 + math.ceil(rows * (C // G) / 32) + 5 + math.ceil(blocks / 32) + 5
+
+
+@pytest.mark.parametrize("shape,groups,dtype,offset", [
+    ((148, 6000, 64), 8, torch.float32, 0.5), ((160, 3000, 32), 4, torch.bfloat16, 0.0), ((75, 9000, 64), 8, torch.float32, 30.0),
+    ((149, 2001, 128), 32, torch.float16, 2.0), ((148, 700, 8), 2, torch.float32, 1000.0),
+])
+def test_group_norm_many_samples(shape, groups, dtype, offset):
+    Bn, S, C = shape
+    x = (torch.randn(shape, generator=torch.Generator("cuda").manual_seed(68), device="cuda") + offset).to(dtype)
+    w, b = (1 + 0.2 * torch.randn(C, generator=gen(69))).cuda(), (0.2 * torch.randn(C, generator=gen(70))).cuda()
+    y, mean, rstd = w8a8.group_norm(x, groups, w, b, return_stats=True)
+    n = joins(Bn, S, C, groups, dtype)
+    for lo in range(0, Bn, 40):
+        part = slice(lo, lo + 40)
+        xg = x[part].double().view(-1, S, groups, C // groups)
+        m64 = xg.mean((1, 3))
+        r64 = 1 / torch.sqrt(((xg - m64[:, None, :, None]) ** 2).mean((1, 3)) + 1e-5)
+        off = m64.abs() + 1 / r64
+        close(mean[part], m64.cpu(), (n * U * off).cpu(), "mean")
+        # deviations are off by U of the mean each and once per join
+        close(rstd[part], r64.cpu(), (n * U * r64 * (1 + n * U * (off * r64) ** 2)).cpu(), "rstd")
+        xh = ((xg - m64[:, None, :, None]) * r64[:, None, :, None])
+        slack = U * (n * (1 + xh.abs() + (off * r64)[:, None, :, None])).reshape(-1, S, C) * w.double() + 4 * U * b.double().abs()
+        close(y[part], (xh.reshape(-1, S, C) * w.double() + b.double()).cpu(), slack.cpu(), "y")
+
+
 @pytest.mark.parametrize("fill", [0x00, 0xFF, 0x5A])
 def test_group_norm_workspace_contents_do_not_matter(fill):
     x, w, b, (xd, wd, bd) = make_norm((2, 3000, 64), torch.bfloat16, "same", 0.0)

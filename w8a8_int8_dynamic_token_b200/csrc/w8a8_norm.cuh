@@ -29,10 +29,12 @@
 //
 // Statistics: a thread keeps one 16-byte vector of channels; batches of rows
 // are reduced in two passes over registers (mean, then squared deviations)
-// and joined by the pairwise update of Chan, Golub and LeVeque (1979).  No
-// difference of large squares appears, so a mean far from zero costs no
-// precision.  All joins run in a fixed order (no atomics on sums): equal
-// inputs give equal bits.
+// and joined by the pairwise update of Chan, Golub and LeVeque (1979), which
+// takes no difference of large squares.  The mean itself, of a thread and of the
+// group, is one fp32 value, off by some 2^-24 of its size per join, and x - mean
+// is off by as much: a group whose mean is m standard deviations from zero
+// loses about log2(m) bits.  All joins run in a fixed order (no atomics on
+// sums): equal inputs give equal bits.
 //
 // The blocks of a sample exchange (mean, squared deviations) or the gradient's
 // two sums per group through 16-byte entries that carry their launch's tag and
