@@ -139,10 +139,11 @@ __global__ void __launch_bounds__(kGradThreads)
 // it is still under way; the barrier's parity alone would then let it through.
 // It therefore waits until the row's own copy has been asked for (`issued`),
 // which happens once the copy before it has landed, and only then for its phase.
-// 4352 x 12288 takes 37 us (160 MB of traffic: 28.7 as a bare stream of the same
-// reads and writes), bound by shared memory: 12 bytes an element, 18 us of it.
+// 4352 x 12288 takes 41 us in a capture (160 MB of traffic: 28.7 as a bare stream
+// of the same reads and writes), bound by shared memory: 12 bytes an element, 18
+// us of it; the count of copies is 2% (8704 x 8192, whole calls: 74.3 and 72.9).
 // With the scales in registers instead (whole block on two rows at a time, one
-// barrier per two rows) it took 38, with two such teams 46.
+// barrier per two rows) it took 38 where this took 37, with two such teams 46.
 constexpr int kGradBulkWarps = 16;
 constexpr int kGradMaxSlots = 16;
 
