@@ -33,7 +33,8 @@
 // takes no difference of large squares.  The mean itself, of a thread and of the
 // group, is one fp32 value, off by some 2^-24 of its size per join, and x - mean
 // is off by as much: a group whose mean is m standard deviations from zero
-// loses about log2(m) bits.  All joins run in a fixed order (no atomics on
+// loses about log2(m) bits (of rstd, too, where it has few values; over many
+// the joins' errors cancel).  All joins run in a fixed order (no atomics on
 // sums): equal inputs give equal bits.
 //
 // The blocks of a sample exchange (mean, squared deviations) or the gradient's
