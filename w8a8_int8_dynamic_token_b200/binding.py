@@ -751,12 +751,13 @@ def rotary(x, positions, inv_freq, k=None, layout="interleaved", axis=None, scal
     dim] (and, in the same launch, on k with its own number of heads); bf16,
     fp16 or fp32, any strides outside a head.  inv_freq: CPU float64 [rot / 2]
     radians per position, at least 0 and below 2^64 (see rotary_frequencies);
-    the first rot values of a head turn, the others are copied.  positions: int32 or int64 on x's device,
-    [tokens] or [batch, tokens], or with a last dimension of axes when `axis`
-    (CPU int32 [rot / 2], the axis of each pair) is given.  backward=True: the
-    gradient.  out / out_k: where to write; x / k themselves, or memory that
-    does not overlap them.  Returns y, or (y, y_k) with k, laid out as x and k
-    where those are dense."""
+    the first rot values of a head turn, the others are copied.  positions:
+    int32 or int64 on x's device, [tokens] or [batch, tokens], or with a last
+    dimension of axes when `axis` (CPU int32 [rot / 2], the axis of each pair) is
+    given.  backward=True: the gradient.  out / out_k: where to write; x / k
+    themselves, or memory that does not overlap them, each head a place of its
+    own.  Returns y, or (y, y_k) with k, laid out as x and k where those are
+    dense."""
     _heads(x, "x", None)
     dtype = x.dtype
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or \
